@@ -64,7 +64,10 @@ enum {
   SWIMBA_OP_SEPARATE = 6, /* swimba_separate_scan */
   SWIMBA_OP_SCAN_BWD = 7,  /* swimba_scan_bwd */
   SWIMBA_OP_PROJ_BWD = 8,  /* swimba_proj_bwd */
-  SWIMBA_OP_ROUTE_BWD = 9  /* swimba_route_bwd */
+  SWIMBA_OP_ROUTE_BWD = 9, /* swimba_route_bwd */
+  /* for swimba_linattn_workspace_size */
+  SWIMBA_OP_LINATTN_FWD = 10, /* swimba_linattn_fwd */
+  SWIMBA_OP_LINATTN_BWD = 11  /* swimba_linattn_bwd */
 };
 
 typedef struct {
@@ -427,6 +430,130 @@ swimba_status swimba_block_fwd(const swimba_block_dims *bd, const void *u,
 swimba_status swimba_block_step(const swimba_block_dims *bd, const void *u,
                                 const swimba_block_weights *w, float *h, void *conv_state,
                                 void *out, void *ws, size_t ws_bytes, void *stream);
+
+/* ---- Linear attention with a decay for each head ----------------------------------------------
+ * The mixer of the SSD form above with queries and keys of each head's own and one fixed decay per
+ * head. Per head h a state S [d_k, d_v], all arithmetic on it in fp32:
+ *   S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T          o_t = scale S_t^T q_t
+ * n_kv_heads divides n_heads: query head h reads k and v of head h / (n_heads / n_kv_heads)
+ * (n_kv_heads = n_heads: every head has its own); every query head keeps its own state and decay.
+ * d_k, d_v: multiples of 8, at most 128. log_decay <= 0 (0: no decay; -infinity: each token sees
+ * only itself); it is a constant of the head, no gradient is taken with respect to it.
+ * q, k and v may be columns of one projection's output: q_stride, k_stride, v_stride are the
+ * distances in elements from one token to the next (multiples of 8, at least n_heads d_k,
+ * n_kv_heads d_k, n_kv_heads d_v); heads are contiguous inside a token's row, and a sequence's
+ * tokens follow the previous sequence's. The other tensors are dense.
+ * bf16: chunks of 128 tokens on the tensor cores; the masked, decayed scores and the state's copy
+ * for the readout are rounded to bf16 once each, everything that is carried on stays fp32 (values
+ * enter the state update as three bf16 parts, together exact to 24 bits). fp32: the recurrence in
+ * fp32 on the SIMT cores. A value that is not finite may spread to every output of its chunk of 128
+ * tokens and to what follows it in its sequence, never to another sequence. */
+typedef struct {
+  int64_t batch;      /* B */
+  int64_t seqlen;     /* L (1 for swimba_linattn_step) */
+  int32_t n_heads;    /* H */
+  int32_t n_kv_heads; /* Hkv */
+  int32_t d_k;
+  int32_t d_v;
+  int64_t q_stride; /* elements from one token's q to the next */
+  int64_t k_stride;
+  int64_t v_stride;
+  int32_t io_dtype; /* swimba_dtype of q, k, v, o and their gradients */
+  float scale;      /* multiplies o */
+} swimba_linattn_dims;
+
+/* Bytes of device workspace `op` (SWIMBA_OP_LINATTN_FWD or _BWD) needs: 0 on invalid dims. The first
+ * 256 bytes are the status block; zero the workspace once after allocating it. */
+size_t swimba_linattn_workspace_size(const swimba_linattn_dims *dims, int op);
+
+/* Whole sequences.
+ *   q [B, L, H, d_k], k [B, L, Hkv, d_k], v [B, L, Hkv, d_v] io, token strides as in dims   (in)
+ *   log_decay [H] fp32                                                                      (in)
+ *   lens    [B] int32 tokens of each sequence (values outside 0 .. L count as the nearer of the
+ *           two), or NULL: all L. Tokens at or after a sequence's length are not used, whatever
+ *           they hold, and their rows of o are left as they were                            (in)
+ *   S0      [B, H, d_k, d_v] fp32 starting state, or NULL for zeros                         (in)
+ *   o       [B, L, H, d_v] io                                                               (out)
+ *   S_final [B, H, d_k, d_v] fp32 state after the last token, or NULL (may be S0)           (out)
+ *   ws: at least swimba_linattn_workspace_size(dims, SWIMBA_OP_LINATTN_FWD) bytes. */
+swimba_status swimba_linattn_fwd(const swimba_linattn_dims *dims, const void *q, const void *k,
+                                 const void *v, const float *log_decay, const int32_t *lens,
+                                 const float *S0, void *o, float *S_final, void *ws, size_t ws_bytes,
+                                 void *stream);
+
+/* One decode token per sequence (dims->seqlen must be 1), on the SIMT cores in fp32 for both types.
+ *   S_in, S_out [B, H, d_k, d_v] fp32: the state before and after the token; may be one buffer. */
+swimba_status swimba_linattn_step(const swimba_linattn_dims *dims, const void *q, const void *k,
+                                  const void *v, const float *log_decay, const float *S_in, void *o,
+                                  float *S_out, void *stream);
+
+/* Backward pass of swimba_linattn_fwd: with the state's adjoint
+ *   G_t = scale q_t g_o,t^T + exp(log_decay[h]) G_{t+1}   (G past the last token: g_S, undecayed)
+ *   dq_t = scale S_t g_o,t;  dk_t = G_t v_t;  dv_t = G_t^T k_t;  dS0 = exp(log_decay[h]) G_0
+ * (dS0 = g_S for an empty sequence). dk and dv of a shared head sum over the query heads that read
+ * it, in a fixed order.
+ *   q, k, v, log_decay, lens, S0: the forward's                                             (in)
+ *   g_o [B, L, H, d_v] io = dL/do (rows at or after a sequence's length are not used)       (in)
+ *   g_S [B, H, d_k, d_v] fp32 = dL/dS_final, or NULL for zeros                              (in)
+ *   dq, dk, dv io, laid out as q, k and v are (the same token strides); zeros in the rows at or
+ *   after a sequence's length                                                               (out)
+ *   dS0 [B, H, d_k, d_v] fp32, or NULL (not g_S or S0)                                      (out)
+ *   The states are recomputed, nothing of the forward call is read.
+ *   ws: at least swimba_linattn_workspace_size(dims, SWIMBA_OP_LINATTN_BWD) bytes. */
+swimba_status swimba_linattn_bwd(const swimba_linattn_dims *dims, const void *q, const void *k,
+                                 const void *v, const float *log_decay, const int32_t *lens,
+                                 const float *S0, const void *g_o, const float *g_S, void *dq, void *dk,
+                                 void *dv, float *dS0, void *ws, size_t ws_bytes, void *stream);
+
+/* ---- The norms around a block, with its gate and residual ---------------------------------------
+ * What lies between a block's mixer output y and the next block's input, in one pass over the rows
+ * (one row per token, `width` channels; every part but y or res is optional):
+ *   a = y SiLU(z)                                     the gate (z NULL: a = y)
+ *   p = a / sqrt(mean(a^2) + eps) w_post              norm after the mixer, the mean over each of
+ *                                                     `groups` equal parts of the row (w_post NULL: p = a)
+ *   h = res_scale res + out_scale p                   the residual stream (res NULL: h = out_scale p;
+ *                                                     y NULL: h = res_scale res)
+ *   n = h / sqrt(mean(h^2) + eps) w_pre               norm before the next block
+ * With gate_last = 1 the gate follows the norm: p = y / sqrt(mean(y^2) + eps) w_post SiLU(z). All
+ * arithmetic is fp32; n is taken from h before h is rounded to res_dtype. */
+typedef struct {
+  int64_t rows;      /* tokens */
+  int32_t width;     /* channels: a multiple of 8, at most 16384 */
+  int32_t groups;    /* parts of the row the norm after the mixer works on; width / groups % 8 == 0 */
+  int32_t io_dtype;  /* swimba_dtype of y, z, n and their gradients */
+  int32_t res_dtype; /* swimba_dtype of res, h and their gradients */
+  int32_t gate_last; /* 0 or 1 */
+  float eps;         /* > 0 */
+  float res_scale;
+  float out_scale;
+} swimba_norm_dims;
+
+/*   y [rows, width] io, or NULL (then z and w_post must be NULL and res given); z [rows, width] io
+ *   or NULL; w_post [width] fp32 or NULL; res [rows, width] res_dtype or NULL               (in)
+ *   w_pre [width] fp32: required with n, NULL without                                       (in)
+ *   h [rows, width] res_dtype or NULL (may be res); n [rows, width] io or NULL (may be y or z, not
+ *   h); at least one of the two                                                             (out) */
+swimba_status swimba_block_norm_fwd(const swimba_norm_dims *dims, const void *y, const void *z,
+                                    const float *w_post, const void *res, const float *w_pre, void *h,
+                                    void *n, void *stream);
+
+/* Bytes of device workspace swimba_block_norm_bwd needs (0 on invalid dims). */
+size_t swimba_block_norm_workspace_size(const swimba_norm_dims *dims);
+
+/* Backward pass of swimba_block_norm_fwd; everything the forward computed is computed again.
+ *   y, z, w_post, res, w_pre: the forward's                                                 (in)
+ *   g_h [rows, width] res_dtype = dL/dh from the later uses of h, or NULL for zeros          (in)
+ *   g_n [rows, width] io = dL/dn: required with w_pre, NULL without                          (in)
+ *   dy, dz [rows, width] io, dres [rows, width] res_dtype: required where y, z, res are given, NULL
+ *   elsewhere; dres may be g_h, dy may be g_n or y, dz may be z                              (out)
+ *   dw_post, dw_pre [width] fp32: required where w_post, w_pre are given, NULL elsewhere; summed over
+ *   the rows in a fixed order                                                               (out)
+ *   ws: at least swimba_block_norm_workspace_size(dims) bytes. */
+swimba_status swimba_block_norm_bwd(const swimba_norm_dims *dims, const void *y, const void *z,
+                                    const float *w_post, const void *res, const float *w_pre,
+                                    const void *g_h, const void *g_n, void *dy, void *dz, void *dres,
+                                    float *dw_post, float *dw_pre, void *ws, size_t ws_bytes,
+                                    void *stream);
 
 /* Synchronises `stream`, returns the device status recorded in the workspace's status block
  * (SWIMBA_OK or SWIMBA_ERR_TIMEOUT) and clears it. */

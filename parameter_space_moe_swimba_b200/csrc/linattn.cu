@@ -1,0 +1,516 @@
+// Linear attention with a decay for each head: C ABI entry points, the fp32 recurrence, the decode
+// step and the small kernels around them (segment chain, shared-head sums, zero rows).
+//
+// Sources: "Swimba: Switch Mamba Model Scales State Space Models", Dutch summary §2 "Architectuur
+// Implementatie" (the chunked processing of the state space dual form carries over) and "Mamba y las
+// SSMs", "Estado interno puramente lineal" (a linear state can be cut into pieces and recombined);
+// the recurrence itself is stated in include/swimba.h.
+#include <algorithm>
+#include <cstdio>
+
+#include "linattn.cuh"
+
+namespace swimba {
+swimba_status api_cuda_status(cudaError_t e);
+
+namespace {
+
+constexpr int kSimtTokens = 16;   // tokens staged per step
+constexpr int kSimtCols = 64;     // columns of M per CTA
+constexpr int kSMs = 148;
+
+template <typename IO>
+__device__ __forceinline__ const IO* la_row(const LaStream& s, int b, int64_t t, int h, int d) {
+  return reinterpret_cast<const IO*>(s.p) + b * s.sb + t * s.st + (int64_t)(h / s.div) * d;
+}
+
+// ---- the recurrence, token by token ------------------------------------------------------------------
+// One CTA of 128 threads per (role, sequence, head, segment, 64 columns of M). A thread keeps NI x 4
+// rows (16 i + 4 p + 0..3, p its quarter) of two columns in registers, so a token costs it 3 FMA-pipe
+// operations per state element and one 16-byte shared read of x and of y per 8 of them; the four
+// quarters' partial readouts meet in two shuffles. Bound by the FMA pipe (3 d_x d_w operations per
+// token and head). MODE 0 writes the outputs, MODE 1 only the segment's end state from zero.
+template <typename IO, int NI, int MODE>
+__global__ void __launch_bounds__(128) la_simt_kernel(const __grid_constant__ LaParams p) {
+  __shared__ __align__(16) float sx[kSimtTokens][NI * 16];
+  __shared__ __align__(16) float sy[kSimtTokens][NI * 16];
+  __shared__ __align__(16) float sw[kSimtTokens][kSimtCols];
+  __shared__ __align__(16) float so[MODE == 0 ? kSimtTokens : 1][kSimtCols];
+  const int tid = threadIdx.x, lane = tid & 31, part = lane & 3;
+  const int col = (tid >> 5) * 16 + (lane >> 2) * 2;
+  int64_t item = blockIdx.x;
+  const int seg = (int)(item % p.nseg);
+  item /= p.nseg;
+  const int64_t bh = item % ((int64_t)p.B * p.H);
+  const LaRole& r = p.role[item / ((int64_t)p.B * p.H)];
+  const int b = (int)(bh / p.H), h = (int)(bh % p.H);
+  const int c_base = blockIdx.y * kSimtCols;
+  if (c_base >= r.dw) return;
+  const int ncol = min(kSimtCols, r.dw - c_base);
+  const float lg = p.g[h] * kLog2e, gamma = la_pow(lg, 1);
+  const int64_t len = la_len(p, b);
+  int c0, c1;
+  la_segment(p, len, seg, r.rev, c0, c1);
+  const int64_t lo = (int64_t)c0 * kLaChunk, hi = min((int64_t)c1 * kLaChunk, len);
+
+  float M[NI * 4][2];
+  const float* start = p.nseg > 1 ? r.seg + (bh * p.nseg + seg) * r.dx * r.dw : r.M0 ? r.M0 + bh * r.dx * r.dw : nullptr;
+  const int sj = p.nseg > 1 ? r.dw : r.sj, sc = p.nseg > 1 ? 1 : r.sc;
+#pragma unroll
+  for (int i = 0; i < NI * 4; ++i) {
+    const int j = 16 * (i >> 2) + 4 * part + (i & 3);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      M[i][e] = (MODE == 0 && start != nullptr && j < r.dx && col + e < ncol)
+                    ? start[(int64_t)j * sj + (int64_t)(c_base + col + e) * sc]
+                    : 0.f;
+  }
+  for (int i = tid; i < kSimtTokens * NI * 16; i += 128) {  // the padding stays zero
+    sx[0][i] = 0.f;
+    sy[0][i] = 0.f;
+  }
+  for (int i = tid; i < kSimtTokens * kSimtCols; i += 128) sw[0][i] = 0.f;
+
+  constexpr int V = Vec16<IO>::n;
+  float decay = r.rev ? 1.f : gamma;  // before a token; M is already decayed to a reverse segment's first token
+  for (int64_t at = 0; at < hi - lo; at += kSimtTokens) {
+    const int n = (int)min((int64_t)kSimtTokens, hi - lo - at);
+    auto token = [&](int i) { return r.rev ? hi - 1 - at - i : lo + at + i; };
+    __syncthreads();
+    auto stage = [&](const LaStream& s, float* dst, int pitch, int first, int count, int d, float f) {
+      const int per = count / V;
+      for (int i = tid; i < n * per; i += 128) {
+        const int t = i / per, v = (i - t * per) * V;
+        float f8[V];
+        Vec16<IO>::unpack(*reinterpret_cast<const uint4*>(la_row<IO>(s, b, token(t), h, d) + first + v), f8);
+#pragma unroll
+        for (int e = 0; e < V; ++e) dst[t * pitch + v + e] = f8[e] * f;
+      }
+    };
+    if (MODE == 0) stage(r.x, sx[0], NI * 16, 0, r.dx, r.dx, 1.f);
+    stage(r.y, sy[0], NI * 16, 0, r.dx, r.dx, 1.f);
+    stage(r.w, sw[0], kSimtCols, c_base, ncol, r.dw, r.s_u);
+    __syncthreads();
+    for (int t = 0; t < n; ++t) {
+      const float2 w = *reinterpret_cast<const float2*>(&sw[t][col]);
+      float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const float4 y = *reinterpret_cast<const float4*>(&sy[t][16 * i + 4 * part]);
+        const float yv[4] = {y.x, y.y, y.z, y.w};
+        float xv[4] = {};
+        if (MODE == 0) {
+          const float4 x = *reinterpret_cast<const float4*>(&sx[t][16 * i + 4 * part]);
+          xv[0] = x.x, xv[1] = x.y, xv[2] = x.z, xv[3] = x.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float* m = M[4 * i + e];
+          m[0] = fmaf(yv[e], w.x, m[0] * decay);
+          m[1] = fmaf(yv[e], w.y, m[1] * decay);
+          if (MODE == 0) {
+            a0 = fmaf(xv[e], m[0], a0);
+            a1 = fmaf(xv[e], m[1], a1);
+          }
+        }
+      }
+      decay = gamma;
+      if (MODE == 0) {
+        a0 += __shfl_xor_sync(0xffffffffu, a0, 1);
+        a1 += __shfl_xor_sync(0xffffffffu, a1, 1);
+        a0 += __shfl_xor_sync(0xffffffffu, a0, 2);
+        a1 += __shfl_xor_sync(0xffffffffu, a1, 2);
+        if (part == 0) *reinterpret_cast<float2*>(&so[t][col]) = make_float2(a0 * r.s_inter, a1 * r.s_inter);
+      }
+    }
+    if (MODE == 0) {
+      __syncthreads();
+      for (int i = tid; i < n * ncol; i += 128) {
+        const int t = i / ncol, c = i - t * ncol;
+        const int64_t at_out = b * r.out_sb + token(t) * r.out_st + (int64_t)h * r.dw + c_base + c;
+        if (r.out_f32) reinterpret_cast<float*>(r.out)[at_out] = so[t][c];
+        else from_f32(reinterpret_cast<IO*>(r.out)[at_out], so[t][c]);
+      }
+    }
+  }
+  if (MODE == 0 && (p.nseg > 1 || r.M_end == nullptr)) return;
+  // a reverse segment leaves M decayed to the token before it (`decay` is γ once a token was seen)
+  const float last = r.rev ? decay : 1.f;
+  float* end = MODE == 1 ? r.seg + (bh * p.nseg + seg) * r.dx * r.dw : r.M_end + bh * r.dx * r.dw;
+  const int ej = MODE == 1 ? r.dw : r.sj, ec = MODE == 1 ? 1 : r.sc;
+#pragma unroll
+  for (int i = 0; i < NI * 4; ++i) {
+    const int j = 16 * (i >> 2) + 4 * part + (i & 3);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (j < r.dx && col + e < ncol) end[(int64_t)j * ej + (int64_t)(c_base + col + e) * ec] = M[i][e] * last;
+  }
+}
+
+// ---- segment chain -------------------------------------------------------------------------------------
+// seg[s] holds segment s's end state from zero; it becomes the state before segment s, and the state
+// after the last one goes to M_end. One thread per state element.
+__global__ void __launch_bounds__(256) la_chain_kernel(const __grid_constant__ LaParams p) {
+  const int64_t item = blockIdx.x, bhs = (int64_t)p.B * p.H;
+  const LaRole& r = p.role[item / bhs];
+  const int64_t bh = item % bhs;
+  const int b = (int)(bh / p.H), h = (int)(bh % p.H), size = r.dx * r.dw;
+  const int e = blockIdx.y * 256 + threadIdx.x;
+  if (e >= size) return;
+  const int j = e / r.dw, c = e - j * r.dw;
+  const float lg = p.g[h] * kLog2e;
+  const int64_t len = la_len(p, b);
+  float* seg = r.seg + bh * p.nseg * size + e;
+  const int64_t own = bh * size + (int64_t)j * r.sj + (int64_t)c * r.sc;
+  float m = r.M0 ? r.M0[own] : 0.f;
+  for (int s = 0; s < p.nseg; ++s) {
+    int c0, c1;
+    la_segment(p, len, s, r.rev, c0, c1);
+    const int64_t n = max((int64_t)0, min((int64_t)c1 * kLaChunk, len) - (int64_t)c0 * kLaChunk);
+    const float end = seg[(int64_t)s * size];
+    seg[(int64_t)s * size] = m;
+    if (n > 0) m = fmaf(la_pow(lg, (int)n), m, end);
+  }
+  if (r.M_end) r.M_end[own] = m;
+}
+
+// ---- rows without a token, shared heads ----------------------------------------------------------------
+// out[b, t, kv, :] = Σ_i part[b, t, kv group + i, :] for tokens inside the sequence (fixed order), zeros
+// in the rows behind it; with part == null only the zeros are written. One thread per 8 elements.
+template <typename IO>
+__global__ void __launch_bounds__(256) la_rows_kernel(IO* out, int64_t st, int64_t sb, const float* part, int group,
+                                                      int width, int d, int64_t L, const int32_t* lens, int64_t total) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= total) return;
+  const int per = width / 8;
+  const int64_t row = i / per, b = row / L, t = row - b * L;
+  const int at = (int)(i - row * per) * 8;
+  const bool live = lens == nullptr || t < (int64_t)lens[b];
+  if (live && part == nullptr) return;
+  float v[8] = {};
+  if (live) {
+    const int kv = at / d, j = at - kv * d;
+    const float* src = part + (row * (width / d) * group + (int64_t)kv * group) * d + j;
+    for (int g = 0; g < group; ++g)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += src[(int64_t)g * d + e];
+  }
+  IO* dst = out + b * sb + t * st + at;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) from_f32(dst[e], v[e]);
+}
+
+// ---- decode step ----------------------------------------------------------------------------------------
+// One CTA per (sequence, head): the state is read and written once (8 d_k d_v bytes), which bounds it.
+// Threads go over the state row by row, 16 bytes each; the partial readouts of the threads that share
+// columns meet in shared memory.
+template <typename IO>
+__global__ void __launch_bounds__(256) la_step_kernel(LaStream q, LaStream k, LaStream v, const float* g,
+                                                      const float* S_in, IO* o, float* S_out, int H, int dk, int dv,
+                                                      float scale) {
+  __shared__ float sq[128], sk[128];
+  __shared__ __align__(16) float red[1024];
+  const int64_t bh = blockIdx.x;
+  const int b = (int)(bh / H), h = (int)(bh % H), tid = threadIdx.x;
+  const int c4 = dv / 4, R = 256 / c4, r0 = tid / c4, c = tid - r0 * c4;
+  if (tid < dk) {
+    sq[tid] = to_f32(la_row<IO>(q, b, 0, h, dk)[tid]) * scale;
+    sk[tid] = to_f32(la_row<IO>(k, b, 0, h, dk)[tid]);
+  }
+  const float gamma = la_pow(g[h] * kLog2e, 1);
+  __syncthreads();
+  if (r0 < R) {
+    const IO* vp = la_row<IO>(v, b, 0, h, dv) + 4 * c;
+    const float4 vv = make_float4(to_f32(vp[0]), to_f32(vp[1]), to_f32(vp[2]), to_f32(vp[3]));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4* in = reinterpret_cast<const float4*>(S_in + bh * dk * dv);
+    float4* out = reinterpret_cast<float4*>(S_out + bh * dk * dv);
+#pragma unroll 8
+    for (int j = r0; j < dk; j += R) {
+      float4 s = in[(int64_t)j * c4 + c];
+      const float kj = sk[j], qj = sq[j];
+      s.x = fmaf(gamma, s.x, kj * vv.x);
+      s.y = fmaf(gamma, s.y, kj * vv.y);
+      s.z = fmaf(gamma, s.z, kj * vv.z);
+      s.w = fmaf(gamma, s.w, kj * vv.w);
+      acc.x = fmaf(qj, s.x, acc.x);
+      acc.y = fmaf(qj, s.y, acc.y);
+      acc.z = fmaf(qj, s.z, acc.z);
+      acc.w = fmaf(qj, s.w, acc.w);
+      out[(int64_t)j * c4 + c] = s;
+    }
+    reinterpret_cast<float4*>(red)[r0 * c4 + c] = acc;
+  }
+  __syncthreads();
+  if (tid < dv) {
+    float a = 0.f;
+    for (int r = 0; r < R; ++r) a += red[r * dv + tid];
+    from_f32(o[bh * dv + tid], a);
+  }
+}
+
+// ---- host -----------------------------------------------------------------------------------------------
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+
+swimba_status check_la(const swimba_linattn_dims* d) {
+  if (d == nullptr || d->batch <= 0 || d->seqlen <= 0 || d->n_heads <= 0 || d->n_kv_heads <= 0 || d->d_k <= 0 ||
+      d->d_v <= 0)
+    return SWIMBA_ERR_INVALID_ARG;
+  if (d->io_dtype != SWIMBA_F32 && d->io_dtype != SWIMBA_BF16) return SWIMBA_ERR_INVALID_ARG;
+  if (d->n_heads % d->n_kv_heads != 0) return SWIMBA_ERR_INVALID_ARG;
+  if (d->d_k % 8 || d->d_v % 8 || d->d_k > 128 || d->d_v > 128) return SWIMBA_ERR_UNSUPPORTED;
+  if (d->n_heads > (1 << 16) || d->batch > (1 << 20) || d->seqlen > (int64_t(1) << 30) ||
+      d->batch * d->n_heads > (1 << 22) || d->batch * d->seqlen > (int64_t(1) << 31))
+    return SWIMBA_ERR_UNSUPPORTED;
+  const int64_t w[3] = {(int64_t)d->n_heads * d->d_k, (int64_t)d->n_kv_heads * d->d_k, (int64_t)d->n_kv_heads * d->d_v};
+  const int64_t st[3] = {d->q_stride, d->k_stride, d->v_stride};
+  for (int i = 0; i < 3; ++i) {
+    if (st[i] < w[i]) return SWIMBA_ERR_INVALID_ARG;
+    if (st[i] % 8 || st[i] > (int64_t(1) << 31) || d->seqlen * st[i] > (int64_t(1) << 38)) return SWIMBA_ERR_UNSUPPORTED;
+  }
+  return SWIMBA_OK;
+}
+
+// Segments per sequence. Splitting a sequence costs a second pass over y and w (the segments' end
+// states), so it pays only where the heads alone leave SMs idle. The rule takes the split with the
+// least time in units of one chunk's outputs on one CTA: rounds of CTAs x chunks per segment, with
+// half a unit more per chunk for the state pass of a split sequence and two units per launch.
+LaPlan la_plan(const swimba_linattn_dims* d, int roles, bool tc) {
+  const int64_t nch = (d->seqlen + kLaChunk - 1) / kLaChunk, heads = d->batch * d->n_heads * roles;
+  const int64_t slots = tc ? kSMs : 4 * kSMs;
+  LaPlan best{tc, 1, (int)nch};
+  double least = (double)((heads + slots - 1) / slots) * nch;
+  for (int64_t n = 2; n <= std::min<int64_t>(nch, 64); ++n) {
+    const int64_t cps = (nch + n - 1) / n, segs = (nch + cps - 1) / cps;
+    const double t = (double)((heads * segs + slots - 1) / slots) * cps * 1.5 + 4;
+    if (t < least) {
+      least = t;
+      best = LaPlan{tc, (int)segs, (int)cps};
+    }
+  }
+  return best;
+}
+
+struct LaLayout {
+  size_t seg[kLaMaxRoles], part_k, part_v, total;
+};
+
+bool la_use_tc(const swimba_linattn_dims*) { return false; }
+
+LaLayout la_layout(const swimba_linattn_dims* d, const LaPlan& pl, int roles) {
+  LaLayout l{};
+  size_t off = kStatusBytes;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = up256(off + bytes);
+    return at;
+  };
+  for (int i = 0; i < roles; ++i)
+    l.seg[i] = pl.nseg > 1 ? take((size_t)d->batch * d->n_heads * pl.nseg * d->d_k * d->d_v * 4) : 0;
+  if (roles > 1 && d->n_kv_heads < d->n_heads) {
+    l.part_k = take((size_t)d->batch * d->seqlen * d->n_heads * d->d_k * 4);
+    l.part_v = take((size_t)d->batch * d->seqlen * d->n_heads * d->d_v * 4);
+  }
+  l.total = off;
+  return l;
+}
+
+template <typename IO, int NI>
+cudaError_t launch_simt(const LaParams& p, int max_dw, cudaStream_t s) {
+  const dim3 grid((unsigned)((int64_t)p.n_roles * p.B * p.H * p.nseg), (unsigned)((max_dw + kSimtCols - 1) / kSimtCols));
+  if (p.nseg > 1) {
+    la_simt_kernel<IO, NI, 1><<<grid, 128, 0, s>>>(p);
+    note_launch();
+    const dim3 cg((unsigned)((int64_t)p.n_roles * p.B * p.H), 64);  // 64 x 256 threads: up to 128 x 128 elements
+    la_chain_kernel<<<cg, 256, 0, s>>>(p);
+    note_launch();
+  }
+  la_simt_kernel<IO, NI, 0><<<grid, 128, 0, s>>>(p);
+  note_launch();
+  return cudaGetLastError();
+}
+
+template <typename IO>
+cudaError_t run_simt(const LaParams& p, cudaStream_t s) {
+  int dx = 0, dw = 0;
+  for (int i = 0; i < p.n_roles; ++i) {
+    dx = std::max(dx, p.role[i].dx);
+    dw = std::max(dw, p.role[i].dw);
+  }
+  if (dx <= 32) return launch_simt<IO, 2>(p, dw, s);
+  if (dx <= 64) return launch_simt<IO, 4>(p, dw, s);
+  return launch_simt<IO, 8>(p, dw, s);
+}
+
+cudaError_t run_roles(const LaParams& p, bool bf16, cudaStream_t s) {
+  return bf16 ? run_simt<__nv_bfloat16>(p, s) : run_simt<float>(p, s);
+}
+
+template <typename IO>
+void launch_rows(void* out, int64_t st, const float* part, int group, int kv, int d, const swimba_linattn_dims* dims,
+                 const int32_t* lens, cudaStream_t s) {
+  const int64_t total = dims->batch * dims->seqlen * kv * d / 8;
+  la_rows_kernel<IO><<<(unsigned)((total + 255) / 256), 256, 0, s>>>(static_cast<IO*>(out), st, st * dims->seqlen, part,
+                                                                    group, kv * d, d, dims->seqlen, lens, total);
+  note_launch();
+}
+
+LaParams la_params(const swimba_linattn_dims* d, const LaPlan& pl, const float* g, const int32_t* lens, void* ws) {
+  LaParams p{};
+  p.g = g;
+  p.lens = lens;
+  p.L = d->seqlen;
+  p.B = (int)d->batch;
+  p.H = d->n_heads;
+  p.nseg = pl.nseg;
+  p.cps = pl.cps;
+  p.status = ws;
+  return p;
+}
+
+LaStream la_stream(const void* p, int64_t stride, int64_t L, int div) { return LaStream{p, stride, stride * L, div}; }
+
+float* at(void* ws, size_t off) { return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + off); }
+
+}  // namespace
+}  // namespace swimba
+
+using namespace swimba;
+
+extern "C" {
+
+size_t swimba_linattn_workspace_size(const swimba_linattn_dims* dims, int op) {
+  if (check_la(dims) != SWIMBA_OK || (op != SWIMBA_OP_LINATTN_FWD && op != SWIMBA_OP_LINATTN_BWD)) return 0;
+  const int roles = op == SWIMBA_OP_LINATTN_FWD ? 1 : 3;
+  return la_layout(dims, la_plan(dims, roles, la_use_tc(dims)), roles).total;
+}
+
+swimba_status swimba_linattn_fwd(const swimba_linattn_dims* dims, const void* q, const void* k, const void* v,
+                                 const float* log_decay, const int32_t* lens, const float* S0, void* o, float* S_final,
+                                 void* ws, size_t ws_bytes, void* stream) {
+  const swimba_status st = check_la(dims);
+  if (st != SWIMBA_OK) return st;
+  if (!q || !k || !v || !log_decay || !o || o == q || o == k || o == v) return SWIMBA_ERR_INVALID_ARG;
+  const LaPlan pl = la_plan(dims, 1, la_use_tc(dims));
+  const LaLayout l = la_layout(dims, pl, 1);
+  if (ws == nullptr || ws_bytes < l.total) return SWIMBA_ERR_WORKSPACE;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(S0) || !aligned16(S_final) ||
+      !aligned16(ws))
+    return SWIMBA_ERR_ALIGN;
+  LaParams p = la_params(dims, pl, log_decay, lens, ws);
+  const int group = dims->n_heads / dims->n_kv_heads;
+  const int64_t L = dims->seqlen, ow = (int64_t)dims->n_heads * dims->d_v;
+  p.n_roles = 1;
+  LaRole& r = p.role[0];
+  r.x = la_stream(q, dims->q_stride, L, 1);
+  r.y = la_stream(k, dims->k_stride, L, group);
+  r.w = la_stream(v, dims->v_stride, L, group);
+  r.out = o;
+  r.out_st = ow;
+  r.out_sb = ow * L;
+  r.dx = dims->d_k;
+  r.dw = dims->d_v;
+  r.s_inter = dims->scale;
+  r.s_u = 1.f;
+  r.M0 = S0;
+  r.M_end = S_final;
+  r.sj = dims->d_v;
+  r.sc = 1;
+  r.seg = pl.nseg > 1 ? at(ws, l.seg[0]) : nullptr;
+  return api_cuda_status(run_roles(p, dims->io_dtype == SWIMBA_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+swimba_status swimba_linattn_step(const swimba_linattn_dims* dims, const void* q, const void* k, const void* v,
+                                  const float* log_decay, const float* S_in, void* o, float* S_out, void* stream) {
+  const swimba_status st = check_la(dims);
+  if (st != SWIMBA_OK) return st;
+  if (dims->seqlen != 1 || !q || !k || !v || !log_decay || !S_in || !o || !S_out || o == q || o == k || o == v)
+    return SWIMBA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(S_in) || !aligned16(S_out))
+    return SWIMBA_ERR_ALIGN;
+  const int group = dims->n_heads / dims->n_kv_heads;
+  const LaStream sq = la_stream(q, dims->q_stride, 1, 1), sk = la_stream(k, dims->k_stride, 1, group),
+                 sv = la_stream(v, dims->v_stride, 1, group);
+  const unsigned grid = (unsigned)(dims->batch * dims->n_heads);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dims->io_dtype == SWIMBA_BF16)
+    la_step_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(sq, sk, sv, log_decay, S_in, static_cast<__nv_bfloat16*>(o),
+                                                      S_out, dims->n_heads, dims->d_k, dims->d_v, dims->scale);
+  else
+    la_step_kernel<float><<<grid, 256, 0, s>>>(sq, sk, sv, log_decay, S_in, static_cast<float*>(o), S_out,
+                                               dims->n_heads, dims->d_k, dims->d_v, dims->scale);
+  note_launch();
+  return api_cuda_status(cudaGetLastError());
+}
+
+swimba_status swimba_linattn_bwd(const swimba_linattn_dims* dims, const void* q, const void* k, const void* v,
+                                 const float* log_decay, const int32_t* lens, const float* S0, const void* g_o,
+                                 const float* g_S, void* dq, void* dk, void* dv, float* dS0, void* ws, size_t ws_bytes,
+                                 void* stream) {
+  const swimba_status st = check_la(dims);
+  if (st != SWIMBA_OK) return st;
+  if (!q || !k || !v || !log_decay || !g_o || !dq || !dk || !dv) return SWIMBA_ERR_INVALID_ARG;
+  if (dS0 != nullptr && (dS0 == g_S || dS0 == S0)) return SWIMBA_ERR_INVALID_ARG;  // another role may still read them
+  const void* const in[4] = {q, k, v, g_o};
+  void* const out[3] = {dq, dk, dv};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 4; ++j)
+      if (out[i] == in[j]) return SWIMBA_ERR_INVALID_ARG;
+    if (out[i] == out[(i + 1) % 3]) return SWIMBA_ERR_INVALID_ARG;
+  }
+  const LaPlan pl = la_plan(dims, 3, la_use_tc(dims));
+  const LaLayout l = la_layout(dims, pl, 3);
+  if (ws == nullptr || ws_bytes < l.total) return SWIMBA_ERR_WORKSPACE;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(g_o) || !aligned16(dq) || !aligned16(dk) ||
+      !aligned16(dv) || !aligned16(S0) || !aligned16(g_S) || !aligned16(dS0) || !aligned16(ws))
+    return SWIMBA_ERR_ALIGN;
+  LaParams p = la_params(dims, pl, log_decay, lens, ws);
+  const int H = dims->n_heads, group = H / dims->n_kv_heads, d_k = dims->d_k, d_v = dims->d_v;
+  const int64_t L = dims->seqlen, ow = (int64_t)H * d_v;
+  const LaStream sq = la_stream(q, dims->q_stride, L, 1), sk = la_stream(k, dims->k_stride, L, group),
+                 sv = la_stream(v, dims->v_stride, L, group), sd = la_stream(g_o, ow, L, 1);
+  const bool shared = group > 1;
+  p.n_roles = 3;
+  for (int i = 0; i < 3; ++i) {  // dq, dk, dv (the roles of linattn.cuh)
+    LaRole& r = p.role[i];
+    r.x = i == 0 ? sd : i == 1 ? sv : sk;
+    r.y = i == 0 ? sv : i == 1 ? sd : sq;
+    r.w = i == 0 ? sk : i == 1 ? sq : sd;
+    r.dx = i == 2 ? d_k : d_v;
+    r.dw = i == 2 ? d_v : d_k;
+    r.rev = i != 0;
+    r.s_inter = i == 0 ? dims->scale : 1.f;
+    r.s_u = i == 0 ? 1.f : dims->scale;
+    r.M0 = i == 0 ? S0 : g_S;
+    r.M_end = i == 2 ? dS0 : nullptr;
+    r.sj = i == 2 ? d_v : 1;
+    r.sc = i == 2 ? 1 : d_v;
+    r.seg = pl.nseg > 1 ? at(ws, l.seg[i]) : nullptr;
+    if (i > 0 && shared) {
+      r.out = at(ws, i == 1 ? l.part_k : l.part_v);
+      r.out_st = (int64_t)H * r.dw;
+      r.out_f32 = 1;
+    } else {
+      r.out = out[i];
+      r.out_st = i == 0 ? dims->q_stride : i == 1 ? dims->k_stride : dims->v_stride;
+    }
+    r.out_sb = r.out_st * L;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool bf16 = dims->io_dtype == SWIMBA_BF16;
+  const cudaError_t e = run_roles(p, bf16, s);
+  if (e != cudaSuccess) return api_cuda_status(e);
+  auto rows = [&](void* dst, int64_t stride, const float* part, int heads, int d) {
+    if (part == nullptr && lens == nullptr) return;
+    if (bf16) launch_rows<__nv_bfloat16>(dst, stride, part, group, heads, d, dims, lens, s);
+    else launch_rows<float>(dst, stride, part, group, heads, d, dims, lens, s);
+  };
+  rows(dq, dims->q_stride, nullptr, H, d_k);
+  rows(dk, dims->k_stride, shared ? at(ws, l.part_k) : nullptr, dims->n_kv_heads, d_k);
+  rows(dv, dims->v_stride, shared ? at(ws, l.part_v) : nullptr, dims->n_kv_heads, d_v);
+  return api_cuda_status(cudaGetLastError());
+}
+
+}  // extern "C"

@@ -28,6 +28,7 @@ SWIMBA_F32 = 0
 SWIMBA_BF16 = 1
 (SWIMBA_OP_ROUTE, SWIMBA_OP_PROJ, SWIMBA_OP_SCAN, SWIMBA_OP_STEP, SWIMBA_OP_LAYER, SWIMBA_OP_SUMMARY,
  SWIMBA_OP_SEPARATE, SWIMBA_OP_SCAN_BWD, SWIMBA_OP_PROJ_BWD, SWIMBA_OP_ROUTE_BWD) = range(10)
+SWIMBA_OP_LINATTN_FWD, SWIMBA_OP_LINATTN_BWD = 10, 11
 
 STATUS = {
     0: "SWIMBA_OK",
@@ -69,6 +70,13 @@ EXPORTED = [
     "swimba_block_workspace_size",
     "swimba_block_fwd",
     "swimba_block_step",
+    "swimba_linattn_workspace_size",
+    "swimba_linattn_fwd",
+    "swimba_linattn_step",
+    "swimba_linattn_bwd",
+    "swimba_block_norm_fwd",
+    "swimba_block_norm_workspace_size",
+    "swimba_block_norm_bwd",
 ]
 
 
@@ -94,6 +102,36 @@ class swimba_ssd_dims(ctypes.Structure):
         ("head_dim", ctypes.c_int32),
         ("d_state", ctypes.c_int32),
         ("top_k", ctypes.c_int32),
+    ]
+
+
+class swimba_linattn_dims(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("seqlen", ctypes.c_int64),
+        ("n_heads", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("d_k", ctypes.c_int32),
+        ("d_v", ctypes.c_int32),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("io_dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class swimba_norm_dims(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("width", ctypes.c_int32),
+        ("groups", ctypes.c_int32),
+        ("io_dtype", ctypes.c_int32),
+        ("res_dtype", ctypes.c_int32),
+        ("gate_last", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("res_scale", ctypes.c_float),
+        ("out_scale", ctypes.c_float),
     ]
 
 
@@ -179,6 +217,22 @@ _lib.swimba_block_step.argtypes = [ctypes.POINTER(swimba_block_dims), _P, ctypes
                                    _P, _P, _P, ctypes.c_size_t, _P]
 _lib.swimba_block_step.restype = ctypes.c_int
 
+_LD, _ND = ctypes.POINTER(swimba_linattn_dims), ctypes.POINTER(swimba_norm_dims)
+_lib.swimba_linattn_workspace_size.argtypes = [_LD, ctypes.c_int]
+_lib.swimba_linattn_workspace_size.restype = ctypes.c_size_t
+_lib.swimba_linattn_fwd.argtypes = [_LD] + [_P] * 9 + [ctypes.c_size_t, _P]
+_lib.swimba_linattn_fwd.restype = ctypes.c_int
+_lib.swimba_linattn_step.argtypes = [_LD] + [_P] * 8
+_lib.swimba_linattn_step.restype = ctypes.c_int
+_lib.swimba_linattn_bwd.argtypes = [_LD] + [_P] * 13 + [ctypes.c_size_t, _P]
+_lib.swimba_linattn_bwd.restype = ctypes.c_int
+_lib.swimba_block_norm_fwd.argtypes = [_ND] + [_P] * 8
+_lib.swimba_block_norm_fwd.restype = ctypes.c_int
+_lib.swimba_block_norm_workspace_size.argtypes = [_ND]
+_lib.swimba_block_norm_workspace_size.restype = ctypes.c_size_t
+_lib.swimba_block_norm_bwd.argtypes = [_ND] + [_P] * 13 + [ctypes.c_size_t, _P]
+_lib.swimba_block_norm_bwd.restype = ctypes.c_int
+
 
 class SwimbaError(RuntimeError):
     def __init__(self, status: int, where: str):
@@ -201,6 +255,17 @@ def _stream(stream) -> int | None:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _elsewhere(*tensors) -> bool:
+    """Whether a tensor lies on another device than the current one, whose stream the call would use."""
+    found = [t.get_device() for t in tensors if isinstance(t, torch.Tensor)]
+    return bool(found) and set(found) != {torch.cuda.current_device()}
+
+
+def _lies_as(stride, t) -> bool:
+    """Whether a gradient [B, L, heads, d] has its input's token stride."""
+    return not isinstance(t, torch.Tensor) or t.shape[1] == 1 or t.stride(1) == stride
 
 
 def check(status: int, where: str = "swimba") -> None:
@@ -364,6 +429,54 @@ def swimba_block_step(bdims, u, bweights, h, conv_state, out, ws, ws_bytes, stre
                                   _ptr(out), _ptr(ws), int(ws_bytes), _stream(stream))
 
 
+def swimba_linattn_workspace_size(dims: swimba_linattn_dims, op: int) -> int:
+    return int(_lib.swimba_linattn_workspace_size(ctypes.byref(dims), op))
+
+
+def swimba_linattn_fwd(dims, q, k, v, log_decay, lens, S0, o, S_final, ws, ws_bytes, stream=None) -> int:
+    if _elsewhere(q, k, v, log_decay, lens, S0, o, S_final, ws):
+        return 1
+    return _lib.swimba_linattn_fwd(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(lens), _ptr(S0),
+                                   _ptr(o), _ptr(S_final), _ptr(ws), int(ws_bytes), _stream(stream))
+
+
+def swimba_linattn_step(dims, q, k, v, log_decay, S_in, o, S_out, stream=None) -> int:
+    if _elsewhere(q, k, v, log_decay, S_in, o, S_out):
+        return 1
+    return _lib.swimba_linattn_step(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(S_in), _ptr(o),
+                                    _ptr(S_out), _stream(stream))
+
+
+def swimba_linattn_bwd(dims, q, k, v, log_decay, lens, S0, g_o, g_S, dq, dk, dv, dS0, ws, ws_bytes, stream=None) -> int:
+    if _elsewhere(q, k, v, log_decay, lens, S0, g_o, g_S, dq, dk, dv, dS0, ws):
+        return 1
+    if not (_lies_as(dims.q_stride, dq) and _lies_as(dims.k_stride, dk) and _lies_as(dims.v_stride, dv)):
+        return 1
+    return _lib.swimba_linattn_bwd(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(lens), _ptr(S0),
+                                   _ptr(g_o), _ptr(g_S), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dS0), _ptr(ws),
+                                   int(ws_bytes), _stream(stream))
+
+
+def swimba_block_norm_fwd(dims, y, z, w_post, res, w_pre, h, n, stream=None) -> int:
+    if _elsewhere(y, z, w_post, res, w_pre, h, n):
+        return 1
+    return _lib.swimba_block_norm_fwd(ctypes.byref(dims), _ptr(y), _ptr(z), _ptr(w_post), _ptr(res), _ptr(w_pre),
+                                      _ptr(h), _ptr(n), _stream(stream))
+
+
+def swimba_block_norm_workspace_size(dims: swimba_norm_dims) -> int:
+    return int(_lib.swimba_block_norm_workspace_size(ctypes.byref(dims)))
+
+
+def swimba_block_norm_bwd(dims, y, z, w_post, res, w_pre, g_h, g_n, dy, dz, dres, dw_post, dw_pre, ws, ws_bytes,
+                          stream=None) -> int:
+    if _elsewhere(y, z, w_post, res, w_pre, g_h, g_n, dy, dz, dres, dw_post, dw_pre, ws):
+        return 1
+    return _lib.swimba_block_norm_bwd(ctypes.byref(dims), _ptr(y), _ptr(z), _ptr(w_post), _ptr(res), _ptr(w_pre),
+                                      _ptr(g_h), _ptr(g_n), _ptr(dy), _ptr(dz), _ptr(dres), _ptr(dw_post), _ptr(dw_pre),
+                                      _ptr(ws), int(ws_bytes), _stream(stream))
+
+
 # ------------------------------------------------------------------------------------------------
 # marshalling helpers: shapes, host arrays -> device tensors, buffers of one layer call
 # ------------------------------------------------------------------------------------------------
@@ -387,6 +500,57 @@ def make_dims(cfg, seqlen=None, batch=None, n_experts=None, top_k=None) -> swimb
         io_dtype=_dtype_code(cfg.io_dtype),
         w_dtype=_dtype_code(cfg.w_dtype),
     )
+
+
+_TORCH_DTYPE = {torch.float32: SWIMBA_F32, torch.bfloat16: SWIMBA_BF16}
+
+
+def _token_stride(t: torch.Tensor) -> int:
+    """Token stride in elements of a [B, L, heads, d] tensor that include/swimba.h's layout covers: heads
+    contiguous inside a row, sequences L rows apart."""
+    B, L, heads, d = t.shape
+    stride = t.stride(1) if L > 1 else (t.stride(0) if B > 1 else heads * d)
+    inner = (d == 1 or t.stride(3) == 1) and (heads == 1 or t.stride(2) == d)
+    if not inner or (B > 1 and t.stride(0) != L * stride):
+        raise SwimbaError(1, f"linear attention tensor of shape {tuple(t.shape)} and strides {t.stride()}")
+    return stride
+
+
+def make_linattn_dims(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: float) -> swimba_linattn_dims:
+    """Dims of q [B, L, H, d_k], k [B, L, Hkv, d_k], v [B, L, Hkv, d_v] as they lie in memory: dense, or
+    columns of one projection's output."""
+    B, L, H, dk = q.shape
+    if k.shape[:2] != (B, L) or k.shape[3] != dk or v.shape[:3] != k.shape[:3] or len({q.dtype, k.dtype, v.dtype}) > 1:
+        raise SwimbaError(1, f"linear attention of q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
+    return swimba_linattn_dims(batch=B, seqlen=L, n_heads=H, n_kv_heads=k.shape[2], d_k=dk, d_v=v.shape[3],
+                               q_stride=_token_stride(q), k_stride=_token_stride(k), v_stride=_token_stride(v),
+                               io_dtype=_TORCH_DTYPE[q.dtype], scale=float(scale))
+
+
+def new_linattn_workspace(dims: swimba_linattn_dims, op: int, device="cuda") -> torch.Tensor:
+    n = swimba_linattn_workspace_size(dims, op)
+    if n == 0:
+        raise SwimbaError(1, "swimba_linattn_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def make_norm_dims(y: torch.Tensor, h: torch.Tensor, groups: int = 1, eps: float = 1e-5, gate_last: bool = False,
+                   res_scale: float = 1.0, out_scale: float = 1.0) -> swimba_norm_dims:
+    """Dims of a block norm whose mixer output looks like ``y`` and residual stream like ``h`` (the last
+    axis is the width)."""
+    if y.shape != h.shape:
+        raise SwimbaError(1, f"block norm of y {tuple(y.shape)} and h {tuple(h.shape)}")
+    width = y.shape[-1]
+    return swimba_norm_dims(rows=y.numel() // max(1, width), width=width, groups=groups, io_dtype=_TORCH_DTYPE[y.dtype],
+                            res_dtype=_TORCH_DTYPE[h.dtype], gate_last=int(gate_last), eps=eps, res_scale=res_scale,
+                            out_scale=out_scale)
+
+
+def new_norm_workspace(dims: swimba_norm_dims, device="cuda") -> torch.Tensor:
+    n = swimba_block_norm_workspace_size(dims)
+    if n == 0:
+        raise SwimbaError(1, "swimba_block_norm_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
 def to_device(stored: np.ndarray, dtype: str, device="cuda", pin=False) -> torch.Tensor:

@@ -1,0 +1,263 @@
+"""Decay linear attention through the C ABI against the fp64 oracle: prompts, single tokens, gradients.
+
+Tolerances. fp32: each of a token's products and sums is off by at most 2^-24 of the terms it adds, and an
+error made at one token is carried on like the state itself, so a result after n tokens with d-long
+readouts is within (2 n + d + 16) 2^-24 of the sum of absolute terms (``mag``). bf16: besides that, the
+kernel rounds a chunk's masked scores, and the state's copy it reads out, to bf16 once (2^-8 of the terms
+they make: ``once``), and the output once (2^-8 of it). The decays are powers that fp32's exp2 gives to
+within 2^-21, on exponents rounded to 2^-24 relative: |log decay| times the distance, itself a factor of
+the term's own decay, e^-x x <= 1, so another 2^-20 of ``mag`` covers them."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from oracle import mixer_oracle as M
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+HALF_BF16 = 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def S():
+    from parameter_space_moe_swimba_b200 import swimba
+
+    return swimba
+
+
+class Case:
+    """Inputs on the GPU (q, k, v possibly columns of one buffer) and the same values in fp64."""
+
+    def __init__(self, seed, B, L, H, KV, dk, dv, dtype, lens=None, start=True, fused=False, decay=None, scale=0.3):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        t = torch.bfloat16 if dtype == "bf16" else torch.float32
+        self.dtype, self.t, self.scale, self.shape = dtype, t, scale, (B, L, H, KV, dk, dv)
+        randn = lambda *s: torch.randn(s, generator=g, device="cuda")
+        self.fused, self.widths = fused, [H * dk, KV * dk, KV * dv]
+        flat = self.rows(lambda w: randn(B, L, w).to(t))
+        self.q, self.k, self.v = flat
+        self.g_o = randn(B, L, H, dv).to(t)
+        self.S0 = randn(B, H, dk, dv) if start else None
+        self.g_S = randn(B, H, dk, dv) if start else None
+        if decay is None:
+            decay = -torch.exp2(torch.linspace(0, -9, H))
+        elif not isinstance(decay, torch.Tensor):
+            decay = torch.full((H,), float(decay))
+        self.g = decay.float().cuda()
+        self.lens = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+        self.np = {n: self.f64(getattr(self, n)) for n in ("q", "k", "v", "g_o", "S0", "g_S", "g")}
+        self.np_lens = None if lens is None else np.array(lens)
+        if lens is not None:  # what lies behind a sequence's end is anybody's
+            for b, n in enumerate(lens):
+                for x in (self.q, self.k, self.v, self.g_o):
+                    x[b, max(0, n):] = float("nan")
+
+    def rows(self, make):
+        B, L, H, KV, dk, dv = self.shape
+        flat = make(sum(self.widths)).split(self.widths, dim=2) if self.fused else [make(w) for w in self.widths]
+        return [x.unflatten(2, s) for x, s in zip(flat, ((H, dk), (KV, dk), (KV, dv)))]
+
+    @staticmethod
+    def f64(x):
+        return None if x is None else x.double().cpu().numpy()
+
+    def dims(self, S):
+        return S.make_linattn_dims(self.q, self.k, self.v, self.scale)
+
+    def forward(self, S, o=None, S_final=None, stream=None):
+        B, L, H, KV, dk, dv = self.shape
+        d = self.dims(S)
+        ws = S.new_linattn_workspace(d, S.SWIMBA_OP_LINATTN_FWD)
+        o = torch.empty(B, L, H, dv, device="cuda", dtype=self.t) if o is None else o
+        S_final = torch.empty(B, H, dk, dv, device="cuda") if S_final is None else S_final
+        S.check(S.swimba_linattn_fwd(d, self.q, self.k, self.v, self.g, self.lens, self.S0, o, S_final, ws, ws.numel(),
+                                     stream))
+        assert S.swimba_get_device_status(ws, stream) == 0
+        return o, S_final
+
+    def backward(self, S):
+        B, L, H, KV, dk, dv = self.shape
+        d = self.dims(S)
+        ws = S.new_linattn_workspace(d, S.SWIMBA_OP_LINATTN_BWD)
+        nan = float("nan")
+        grads = self.rows(lambda w: torch.full((B, L, w), nan, device="cuda", dtype=self.t))
+        dS0 = torch.full((B, H, dk, dv), nan, device="cuda")
+        S.check(S.swimba_linattn_bwd(d, self.q, self.k, self.v, self.g, self.lens, self.S0, self.g_o, self.g_S, *grads,
+                                     dS0, ws, ws.numel()))
+        assert S.swimba_get_device_status(ws) == 0
+        return (*grads, dS0)
+
+    def n(self):
+        return min(self.shape[1], 10 ** 9)
+
+    def close(self, got, want, once, mag, what, out=True):
+        d = max(self.shape[4], self.shape[5])
+        tol = ((2 * self.n() + d + 16) * 2.0 ** -24 + 2.0 ** -20) * mag
+        if out and self.dtype == "bf16":
+            tol = tol + HALF_BF16 * (once + np.abs(want))
+        off = np.abs(got - want) - tol
+        assert (off <= 1e-30).all(), (what, float(off.max()), float(np.abs(got - want).max()))
+
+
+CASES = {
+    # lengths around the chunk of 128, from one token on
+    **{f"L{n}": dict(B=2, L=n, H=2, KV=2, dk=64, dv=64) for n in (1, 2, 31, 127, 128, 129, 256, 300)},
+    # head sizes, equal and unequal, padded inside the tiles
+    **{f"d{a}x{b}": dict(B=1, L=200, H=2, KV=2, dk=a, dv=b)
+       for a, b in ((8, 8), (16, 128), (64, 128), (128, 64), (128, 128), (72, 40), (96, 96), (24, 112))},
+    # shared heads, columns of one buffer
+    "shared": dict(B=2, L=150, H=6, KV=2, dk=64, dv=128, fused=True),
+    "one_kv": dict(B=1, L=140, H=5, KV=1, dk=32, dv=64, fused=True),
+    # padded batches: empty sequences, ends at, before and after a chunk's, lengths out of range
+    "lens": dict(B=7, L=300, H=2, KV=1, dk=64, dv=64, lens=[300, 0, 1, 128, 129, 257, 255]),
+    "lens_out_of_range": dict(B=3, L=130, H=1, KV=1, dk=64, dv=128, lens=[-5, 1000, 130], fused=True),
+    # decays: none, total, strong (the state underflows inside a chunk), tiny
+    **{f"decay{g}": dict(B=1, L=270, H=2, KV=2, dk=64, dv=64, decay=g) for g in (0.0, -float("inf"), -20.0, -1e-6)},
+    # few heads and many chunks: the sequence is split into segments
+    "split": dict(B=1, L=1500, H=1, KV=1, dk=64, dv=64),
+    "split_lens": dict(B=2, L=1700, H=2, KV=1, dk=32, dv=64, lens=[1430, 400]),
+    "no_start": dict(B=2, L=200, H=2, KV=2, dk=128, dv=128, start=False),
+    "split_no_start": dict(B=1, L=1500, H=1, KV=1, dk=128, dv=128, start=False),
+}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", CASES)
+def test_forward(S, name, dtype):
+    c = Case(1, dtype=dtype, **CASES[name])
+    B, L, H, KV, dk, dv = c.shape
+    o = torch.full((B, L, H, dv), 7.0, device="cuda", dtype=c.t)
+    o, S_final = c.forward(S, o)
+    a = c.np
+    r = M.linattn_forward(a["q"], a["k"], a["v"], a["g"], c.scale, c.np_lens, a["S0"])
+    lens = np.full(B, L) if c.np_lens is None else np.clip(c.np_lens, 0, L)
+    got = Case.f64(o)
+    for b in range(B):
+        assert (got[b, lens[b]:] == 7.0).all()
+        got[b, lens[b]:] = 0
+    c.close(got, r.out, r.once, r.mag, "o")
+    c.close(Case.f64(S_final), r.M, None, r.M_mag, "S_final", out=False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", CASES)
+def test_backward(S, name, dtype):
+    c = Case(2, dtype=dtype, **CASES[name])
+    dq, dk, dv, dS0 = (Case.f64(x) for x in c.backward(S))
+    a, KV = c.np, c.shape[3]
+    rq, rk, rv = M.linattn_backward(a["q"], a["k"], a["v"], a["g"], c.scale, a["g_o"], c.np_lens, a["S0"], a["g_S"])
+    c.close(dq, rq.out, rq.once, rq.mag, "dq")
+    for got, r, what in ((dk, rk, "dk"), (dv, rv, "dv")):
+        c.close(got, *(M.sum_shared(x, KV) for x in (r.out, r.once, r.mag)), what)
+    c.close(dS0, rv.M, None, rv.M_mag, "dS0", out=False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 1, 1, 64, 64), (5, 6, 2, 128, 128), (3, 4, 4, 8, 128), (2, 3, 3, 128, 8),
+                                   (2, 2, 1, 96, 24), (300, 2, 2, 64, 128)])
+def test_step(S, shape, dtype):
+    B, H, KV, dk, dv = shape
+    c = Case(3, B, 1, H, KV, dk, dv, dtype, fused=True)
+    o = torch.empty(B, 1, H, dv, device="cuda", dtype=c.t)
+    out = torch.empty_like(c.S0)
+    S.check(S.swimba_linattn_step(c.dims(S), c.q, c.k, c.v, c.g, c.S0, o, out))
+    a = c.np
+    r = M.linattn_forward(a["q"], a["k"], a["v"], a["g"], c.scale, None, a["S0"])
+    c.close(Case.f64(o), r.out, 0, r.mag, "o")
+    c.close(Case.f64(out), r.M, None, r.M_mag, "S", out=False)
+    o2, state = torch.empty_like(o), c.S0.clone()
+    S.check(S.swimba_linattn_step(c.dims(S), c.q, c.k, c.v, c.g, state, o2, state))
+    assert torch.equal(o, o2) and torch.equal(out, state)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_prompt_then_tokens_is_the_longer_prompt(S, dtype):
+    """Prefill of 200 tokens and 60 single tokens from its state, against one prompt of 260."""
+    c = Case(4, 2, 260, 3, 3, 64, 128, dtype)
+    whole, end = c.forward(S)
+    head = Case(4, 2, 260, 3, 3, 64, 128, dtype)
+    head.q, head.k, head.v = (x[:, :200].contiguous() for x in (c.q, c.k, c.v))
+    head.shape = (2, 200, 3, 3, 64, 128)
+    _, state = head.forward(S)
+    a = c.np
+    r = M.linattn_forward(a["q"], a["k"], a["v"], a["g"], c.scale, None, a["S0"])
+    for t in range(200, 260):
+        q, k, v = (x[:, t:t + 1].contiguous() for x in (c.q, c.k, c.v))
+        o = torch.empty(2, 1, 3, 128, device="cuda", dtype=c.t)
+        S.check(S.swimba_linattn_step(S.make_linattn_dims(q, k, v, c.scale), q, k, v, c.g, state, o, state))
+        c.close(Case.f64(o)[:, 0], r.out[:, t], 0, r.mag[:, t], f"token {t}")
+    c.close(Case.f64(state), r.M, None, r.M_mag, "state", out=False)
+    c.close(Case.f64(end), r.M, None, r.M_mag, "S_final", out=False)
+    c.close(Case.f64(whole), r.out, r.once, r.mag, "o")
+
+
+@pytest.mark.parametrize("name", ["lens", "split", "split_lens", "shared"])
+def test_in_place_state_repeats_graphs_and_streams(S, name):
+    """S_final over S0, two runs, a captured and replayed call, and a call on another stream give the same
+    bits (every sum has a fixed order)."""
+    c = Case(5, dtype="bf16", **CASES[name])
+    B, L, H, KV, dk, dv = c.shape
+    o = torch.zeros(B, L, H, dv, device="cuda", dtype=c.t)
+    o, S_final = c.forward(S, o)
+    start = c.S0.clone()
+    o2 = torch.zeros_like(o)
+    c.forward(S, o2, c.S0)
+    assert torch.equal(c.S0, S_final)
+    c.S0 = start
+    live = lambda x: torch.nan_to_num(x.float(), nan=0.0)
+    assert torch.equal(live(o), live(o2))
+    d = c.dims(S)
+    ws = S.new_linattn_workspace(d, S.SWIMBA_OP_LINATTN_FWD)
+    o3, S3 = torch.zeros_like(o), torch.empty_like(S_final)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    call = lambda s: S.check(S.swimba_linattn_fwd(d, c.q, c.k, c.v, c.g, c.lens, c.S0, o3, S3, ws, ws.numel(), s))
+    call(side)
+    side.synchronize()
+    assert torch.equal(live(o3), live(o)) and torch.equal(S3, S_final)
+    o3.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side, capture_error_mode="relaxed"):
+        call(torch.cuda.current_stream())
+    for _ in range(2):
+        S3.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(live(o3), live(o)) and torch.equal(S3, S_final)
+    del graph
+    first = c.backward(S)
+    again = c.backward(S)
+    assert all(torch.equal(x, y) for x, y in zip(first, again))
+
+
+def test_a_value_that_is_not_finite_stays_in_its_sequence(S):
+    c = Case(6, 3, 300, 2, 2, 64, 64, "bf16")
+    clean, end = c.forward(S)
+    c.v[1, 200] = float("nan")
+    c.k[1, 290] = float("inf")
+    o, S_final = c.forward(S)
+    for b in (0, 2):
+        assert torch.equal(o[b], clean[b]) and torch.equal(S_final[b], end[b])
+    assert torch.equal(o[1, :128], clean[1, :128])  # earlier chunks too
+    assert not torch.isfinite(o[1, 200]).any()
+
+
+def test_offsets_past_32_bits(S):
+    """q, k, v as columns of a buffer whose last tokens lie more than 2^31 elements in."""
+    L, width = 300, 2 ** 23
+    free = torch.cuda.mem_get_info()[0]
+    if free < 12 << 30:
+        pytest.skip("needs 6 GB of device memory")
+    buf = torch.zeros(1, L, width, device="cuda", dtype=torch.bfloat16)
+    c = Case(7, 1, L, 1, 1, 64, 64, "bf16")
+    want = c.forward(S)
+    views = [buf[:, :, i * 64:(i + 1) * 64].unflatten(2, (1, 64)) for i in range(3)]
+    for view, x in zip(views, (c.q, c.k, c.v)):
+        view.copy_(x)
+    c.q, c.k, c.v = views
+    got = c.forward(S)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
