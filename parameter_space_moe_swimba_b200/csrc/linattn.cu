@@ -12,6 +12,7 @@
 
 namespace swimba {
 swimba_status api_cuda_status(cudaError_t e);
+cudaError_t run_la_tc(const LaParams& p, bool states, cudaStream_t s);
 
 namespace {
 
@@ -297,7 +298,7 @@ struct LaLayout {
   size_t seg[kLaMaxRoles], part_k, part_v, total;
 };
 
-bool la_use_tc(const swimba_linattn_dims*) { return false; }
+bool la_use_tc(const swimba_linattn_dims* d) { return d->io_dtype == SWIMBA_BF16; }
 
 LaLayout la_layout(const swimba_linattn_dims* d, const LaPlan& pl, int roles) {
   LaLayout l{};
@@ -317,36 +318,62 @@ LaLayout la_layout(const swimba_linattn_dims* d, const LaPlan& pl, int roles) {
   return l;
 }
 
-template <typename IO, int NI>
+void launch_chain(const LaParams& p, cudaStream_t s) {
+  const dim3 grid((unsigned)((int64_t)p.n_roles * p.B * p.H), 64);  // 64 x 256 threads: up to 128 x 128 elements
+  la_chain_kernel<<<grid, 256, 0, s>>>(p);
+  note_launch();
+}
+
+template <int NI>
 cudaError_t launch_simt(const LaParams& p, int max_dw, cudaStream_t s) {
   const dim3 grid((unsigned)((int64_t)p.n_roles * p.B * p.H * p.nseg), (unsigned)((max_dw + kSimtCols - 1) / kSimtCols));
   if (p.nseg > 1) {
-    la_simt_kernel<IO, NI, 1><<<grid, 128, 0, s>>>(p);
+    la_simt_kernel<float, NI, 1><<<grid, 128, 0, s>>>(p);
     note_launch();
-    const dim3 cg((unsigned)((int64_t)p.n_roles * p.B * p.H), 64);  // 64 x 256 threads: up to 128 x 128 elements
-    la_chain_kernel<<<cg, 256, 0, s>>>(p);
-    note_launch();
+    launch_chain(p, s);
   }
-  la_simt_kernel<IO, NI, 0><<<grid, 128, 0, s>>>(p);
+  la_simt_kernel<float, NI, 0><<<grid, 128, 0, s>>>(p);
   note_launch();
   return cudaGetLastError();
 }
 
-template <typename IO>
 cudaError_t run_simt(const LaParams& p, cudaStream_t s) {
   int dx = 0, dw = 0;
   for (int i = 0; i < p.n_roles; ++i) {
     dx = std::max(dx, p.role[i].dx);
     dw = std::max(dw, p.role[i].dw);
   }
-  if (dx <= 32) return launch_simt<IO, 2>(p, dw, s);
-  if (dx <= 64) return launch_simt<IO, 4>(p, dw, s);
-  return launch_simt<IO, 8>(p, dw, s);
+  if (dx <= 32) return launch_simt<2>(p, dw, s);
+  if (dx <= 64) return launch_simt<4>(p, dw, s);
+  return launch_simt<8>(p, dw, s);
 }
 
-cudaError_t run_roles(const LaParams& p, bool bf16, cudaStream_t s) {
-  return bf16 ? run_simt<__nv_bfloat16>(p, s) : run_simt<float>(p, s);
+// The tensor-core kernel takes roles of one padded size (64 or 128) together: all three where d_k and
+// d_v pad alike, else dq and dk, then dv.
+cudaError_t run_tc(const LaParams& p, cudaStream_t s) {
+  auto pad = [](int d) { return d <= 64 ? 64 : 128; };
+  const bool same = p.n_roles < 3 || pad(p.role[2].dx) == pad(p.role[2].dw);
+  LaParams part[2] = {p, p};
+  if (!same) {
+    part[0].n_roles = 2;
+    part[1].n_roles = 1;
+    part[1].role[0] = p.role[2];
+  }
+  if (p.nseg > 1) {
+    for (int i = 0; i < (same ? 1 : 2); ++i) {
+      const cudaError_t e = run_la_tc(part[i], true, s);
+      if (e != cudaSuccess) return e;
+    }
+    launch_chain(p, s);
+  }
+  for (int i = 0; i < (same ? 1 : 2); ++i) {
+    const cudaError_t e = run_la_tc(part[i], false, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaGetLastError();
 }
+
+cudaError_t run_roles(const LaParams& p, bool bf16, cudaStream_t s) { return bf16 ? run_tc(p, s) : run_simt(p, s); }
 
 template <typename IO>
 void launch_rows(void* out, int64_t st, const float* part, int group, int kv, int d, const swimba_linattn_dims* dims,

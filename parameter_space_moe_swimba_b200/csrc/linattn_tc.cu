@@ -1,0 +1,659 @@
+// Linear attention with a decay for each head, in chunks of 128 tokens on the tcgen05 tensor cores
+// (bf16 tensors; the roles are those of linattn.cuh, in forward order here).
+//
+// For a chunk of n <= 128 tokens and the state M [dx, dw] before it, with γ = exp(log_decay):
+//   P[i, s]  = γ^(i-s) (x_i · y_s) for s <= i, else 0          A = X, B = Y        (K = dx)
+//   out_i    = s_intra Σ_s P[i, s] w_s + s_inter γ^(i+1) Mᵀ x_i  A = P, B = W (K = tokens); A = X, B = M
+//   M       <- γ^n M + s_u Σ_s y_s γ^(n-1-s) w_sᵀ              A = (γ w)ᵀ, B = Y    (K = tokens)
+// A reverse role mirrors the exponents: γ^(s-i) for s >= i, γ^(n-1-i), γ^(s+1).
+//
+// Persistent, one CTA per SM; an item is one (role, segment, sequence, head), its chunks in order:
+//   warp 0       TMA loads of the X, Y, W tiles into a ring of stages
+//   warp 1       issues every MMA
+//   warp 2       TMA stores of the finished output tiles
+//   warp 3       the head's table of powers γ^0 .. γ^128
+//   warps 4-7    one row i = TMEM lane each: scores -> P (bf16, in place, the A operand of P W), the
+//                carried state's readout into registers, the sum of both into the W tile, which no
+//                MMA reads any more, and from there to memory
+//   warps 8-11   one column c of M each, in fp32 registers for the whole item: M's bf16 copy for the
+//                readout (the only rounding of M), (γ w)ᵀ as three bf16 parts into tensor memory (a
+//                ring of two 32-token quarters), M <- γ^n M + U
+// Rounded to bf16: P and M's copy, once each, because each meets a bf16 operand and makes a bf16
+// output; γ w enters M as hi + mid + lo, 24 bits together, so that M stays an fp32 state (two parts
+// would put 3e-6 into S_final and dS0, three 1e-7).
+// Tensor memory: scores / P 128 columns, out 128, U dx, the γ w ring 96.
+// Every wait is bounded; a wait that runs out records SWIMBA_ERR_TIMEOUT, and the CTA drains and exits.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "linattn.cuh"
+#include "sm100.cuh"
+
+namespace swimba {
+
+using namespace sm100;
+
+namespace {
+
+constexpr int kTile = kLaChunk * 128;  // 128 tokens x 128 bytes (64 bf16), 128-byte swizzle: 16 KB
+constexpr int kThreads = 384;
+constexpr int kRing = 2, kPart = 16;   // γ w ring: 2 quarters x 3 parts x 16 columns
+constexpr uint32_t kColP = 0, kColO = 128, kColU = 256, kColRing = 384;
+
+enum { kMapX, kMapY, kMapW, kMapOut };
+
+struct LaTcArgs {
+  CUtensorMap map[kLaMaxRoles][4];
+  LaParams p;
+  int64_t items;
+};
+
+template <int DX, int DW, int MODE>
+struct LaSmem {
+  static constexpr int XB = DX / 64, WB = DW / 64;
+  static constexpr int X = 0, Y = MODE == 0 ? XB * kTile : 0, W = Y + XB * kTile;  // inside a stage
+  static constexpr int STAGE = W + WB * kTile;
+  static constexpr int COPY = MODE == 0 ? DX * DW * 2 : 0;  // M's bf16 copy, [dw rows][dx], K-major
+  static constexpr int ROOM = 229376 - COPY;
+  static constexpr int NS = ROOM / STAGE < 4 ? ROOM / STAGE : 4;
+  static constexpr int M = NS * STAGE;
+  static constexpr int POW = M + COPY;              // 2 x 132 floats
+  static constexpr int BAR = POW + 2 * 132 * 4;     // barriers
+  static constexpr int NBAR = 3 * NS + 6 + 2 * kRing + 1 + 4 + 1;
+  static constexpr int MISC = BAR + NBAR * 8;
+  static constexpr int BYTES = MISC + 16;
+  static_assert(NS >= 2, "two stages");
+  static_assert(BYTES + 1024 <= 232448, "shared memory of one CTA");
+};
+
+__device__ __forceinline__ uint32_t swz16(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+__device__ __forceinline__ uint32_t pair(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+struct LaItem {
+  const LaRole* r;
+  int role, b, h, seg, c0, c1;
+  int64_t bh, len;
+};
+
+__device__ __forceinline__ LaItem la_item(const LaParams& p, int64_t item) {
+  LaItem t;
+  t.role = (int)(item % p.n_roles);
+  item /= p.n_roles;
+  t.seg = (int)(item % p.nseg);
+  t.bh = item / p.nseg;
+  t.r = &p.role[t.role];
+  t.b = (int)(t.bh / p.H);
+  t.h = (int)(t.bh % p.H);
+  t.len = la_len(p, t.b);
+  la_segment(p, t.len, t.seg, t.r->rev, t.c0, t.c1);
+  return t;
+}
+
+// First token of the item's chunk number `i` and its count.
+__device__ __forceinline__ int la_chunk(const LaItem& t, int i, int64_t& t0) {
+  t0 = (int64_t)(t.r->rev ? t.c1 - 1 - i : t.c0 + i) * kLaChunk;
+  return (int)min((int64_t)kLaChunk, t.len - t0);
+}
+
+}  // namespace
+
+// MODE 0: outputs (and the end state, where a sequence is one segment). MODE 1: only every segment's
+// end state from zero; needs neither x, nor scores, nor the state's copy.
+template <int DX, int DW, int MODE>
+__global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constant__ LaTcArgs a) {
+  using SM = LaSmem<DX, DW, MODE>;
+  constexpr int NS = SM::NS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* pw_all = reinterpret_cast<float*>(sm + SM::POW);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + SM::BAR);  // [NS] tiles landed
+  uint64_t* empty = full + NS;                                 // [NS] stage free
+  uint64_t* staged = empty + NS;                               // [NS] output tile written
+  uint64_t* sc_full = staged + NS;                             // scores in tensor memory
+  uint64_t* p_ready = sc_full + 1;                             // P written, the readout taken
+  uint64_t* m_ready = p_ready + 1;                             // M's copy written
+  uint64_t* mx_full = m_ready + 1;                             // the readout in tensor memory, the copy free
+  uint64_t* o_full = mx_full + 1;                              // P W in tensor memory, P and the tiles free
+  uint64_t* o_free = o_full + 1;                               // out columns read
+  uint64_t* ring_full = o_free + 1;                            // [kRing]
+  uint64_t* ring_empty = ring_full + kRing;                    // [kRing]
+  uint64_t* u_full = ring_empty + kRing;
+  uint64_t* pw_full = u_full + 1;                              // [2]
+  uint64_t* pw_empty = pw_full + 2;                            // [2]
+  uint64_t* done = pw_empty + 2;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + SM::MISC);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + SM::MISC + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const LaParams& p = a.p;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+      mbar_init(&staged[i], 4);
+    }
+    mbar_init(sc_full, 1);
+    mbar_init(p_ready, 4);
+    mbar_init(m_ready, 4);
+    mbar_init(mx_full, 1);
+    mbar_init(o_full, 1);
+    mbar_init(o_free, 4);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&ring_full[i], 4);
+      mbar_init(&ring_empty[i], 1);
+    }
+    mbar_init(u_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&pw_full[i], 1);
+      mbar_init(&pw_empty[i], MODE == 0 ? 8 : 4);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // The whole warp waits and goes on, or gives up, together.
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+  };
+  auto give_up = [&](int where) {
+    *abort_flag = 1;
+    if (lane == 0) record_device_error(p.status, SWIMBA_ERR_TIMEOUT, where, blockIdx.x, 0);
+  };
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0) {
+      // ---------------- loads ----------------
+      uint32_t it = 0;
+      bool ok = true;
+      for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
+        const LaItem t = la_item(p, item);
+        const CUtensorMap* map = a.map[t.role];
+        for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
+          const int st = it % NS;
+          int64_t t0;
+          la_chunk(t, i, t0);
+          if (!wait(&empty[st], ((it / NS) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            uint8_t* s = sm + st * SM::STAGE;
+            mbar_arrive_expect_tx(&full[st], SM::STAGE);
+#pragma unroll
+            for (int k = 0; k < SM::XB; ++k) {
+              if (MODE == 0) tma_load_4d(s + SM::X + k * kTile, &map[kMapX], &full[st], 64 * k, t.h / t.r->x.div, (int)t0, t.b);
+              tma_load_4d(s + SM::Y + k * kTile, &map[kMapY], &full[st], 64 * k, t.h / t.r->y.div, (int)t0, t.b);
+            }
+#pragma unroll
+            for (int k = 0; k < SM::WB; ++k)
+              tma_load_4d(s + SM::W + k * kTile, &map[kMapW], &full[st], 64 * k, t.h / t.r->w.div, (int)t0, t.b);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) give_up(71);
+      // copies that may still be landing (after an orderly end every one has been waited for)
+      if (*abort_flag) {
+        for (uint32_t k = it > (uint32_t)NS ? it - NS : 0; k < it; ++k) {
+          const uint64_t w0 = globaltimer_ns();
+          while (!mbar_try_wait(&full[k % NS], (k / NS) & 1) && globaltimer_ns() - w0 < kWaitLimitNs) {
+          }
+        }
+      }
+    } else if (warp == 1) {
+      // ---------------- MMAs ----------------
+      constexpr uint32_t id_sc = idesc_bf16(128, 128, false), id_mx = idesc_bf16(128, DW, false),
+                         id_u = idesc_bf16(128, DX, true), id_pw = idesc_bf16(128, DW, true);
+      const uint32_t base = smem_u32(sm), sM = base + SM::M;
+      uint32_t it = 0;
+      bool ok = true;
+      for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
+        const LaItem t = la_item(p, item);
+        for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
+          const int st = it % NS;
+          const uint32_t ph = it & 1;
+          int64_t t0;
+          const int n = la_chunk(t, i, t0);
+          const uint32_t sX = base + st * SM::STAGE + SM::X, sY = base + st * SM::STAGE + SM::Y,
+                         sW = base + st * SM::STAGE + SM::W;
+          if (!(ok = wait(&full[st], (it / NS) & 1))) break;
+          if (n < kLaChunk && t0 + n < p.L) {
+            // tokens behind the sequence's end that lie in memory: whatever they hold, they are zeros here
+            // (behind the tensor's end the copies have filled in zeros)
+            uint8_t* s = sm + st * SM::STAGE + SM::Y;
+            for (int k = lane; k < (kLaChunk - n) * 8 * (SM::XB + SM::WB); k += 32) {
+              const int tile = k / ((kLaChunk - n) * 8), at = k - tile * (kLaChunk - n) * 8;
+              *reinterpret_cast<uint4*>(s + tile * kTile + n * 128 + at * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (MODE == 0) {
+            // scores; P of the chunk before has been read
+            if (it > 0 && !(ok = wait(o_full, ph ^ 1))) break;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+              for (int ks = 0; ks < DX / 16; ++ks) {
+                const uint32_t off = (ks >> 2) * kTile + (ks & 3) * 32;
+                mma_bf16(tmem + kColP, smem_desc(sX + off, 16, 1024, kLayoutSW128),
+                         smem_desc(sY + off, 16, 1024, kLayoutSW128), id_sc, ks > 0);
+              }
+              mma_commit(sc_full);
+            }
+            __syncwarp();
+            // the carried state's readout
+            if (!(ok = wait(m_ready, ph))) break;
+            if (it > 0 && !(ok = wait(o_free, ph ^ 1))) break;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+              for (int ks = 0; ks < DX / 16; ++ks)
+                mma_bf16(tmem + kColO, smem_desc(sX + (ks >> 2) * kTile + (ks & 3) * 32, 16, 1024, kLayoutSW128),
+                         smem_desc(sM + (ks >> 2) * (DW * 128) + (ks & 3) * 32, 16, 1024, kLayoutSW128), id_mx, ks > 0);
+              mma_commit(mx_full);
+            }
+            __syncwarp();
+          }
+          // U = Σ_s (γ w_s) y_sᵀ, 32 tokens at a time
+          for (int qr = 0; qr < 4; ++qr) {
+            const uint32_t slot = qr & 1, use = it * 2 + (qr >> 1);
+            if (!(ok = wait(&ring_full[slot], use & 1))) break;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+              for (int part = 0; part < 3; ++part)
+#pragma unroll
+                for (int k2 = 0; k2 < 2; ++k2)
+                  mma_bf16_ts(tmem + kColU, tmem + kColRing + slot * 3 * kPart + part * kPart + k2 * 8,
+                              smem_desc(sY + (qr * 32 + k2 * 16) * 128, kTile, 1024, kLayoutSW128), id_u,
+                              (qr | part | k2) != 0);
+              mma_commit(&ring_empty[slot]);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (lane == 0) {
+            mma_commit(u_full);
+            if (MODE == 1) mma_commit(&empty[st]);
+          }
+          __syncwarp();
+          if (MODE == 0) {
+            if (!(ok = wait(p_ready, ph))) break;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+              for (int ks = 0; ks < kLaChunk / 16; ++ks)
+                mma_bf16_ts(tmem + kColO, tmem + kColP + ks * 8, smem_desc(sW + ks * 16 * 128, kTile, 1024, kLayoutSW128),
+                            id_pw, ks > 0);
+              mma_commit(o_full);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      if (!ok) give_up(72);
+      // every MMA of the CTA has completed when `done` does
+      if (lane == 0) {
+        mma_commit(done);
+        const uint64_t w0 = globaltimer_ns();
+        while (!mbar_try_wait(done, 0) && globaltimer_ns() - w0 < kWaitLimitNs) {
+        }
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      // ---------------- stores ----------------
+      if (MODE == 0) {
+        uint32_t it = 0;
+        bool ok = true;
+        for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
+          const LaItem t = la_item(p, item);
+          for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
+            const int st = it % NS;
+            int64_t t0;
+            const int n = la_chunk(t, i, t0);
+            if (!(ok = wait(&staged[st], (it / NS) & 1))) break;
+            if (lane == 0) {
+              if (!t.r->out_f32 && (n == kLaChunk || t0 + n == p.L)) {
+#pragma unroll
+                for (int k = 0; k < SM::WB; ++k)
+                  tma_store_4d(&a.map[t.role][kMapOut], sm + st * SM::STAGE + SM::W + k * kTile, 64 * k, t.h, (int)t0, t.b);
+                bulk_commit();
+                bulk_wait_read<0>();
+              }
+              mbar_arrive(&empty[st]);
+            }
+            __syncwarp();
+          }
+        }
+        if (!ok) give_up(73);
+        if (lane == 0) bulk_wait<0>();
+        __syncwarp();
+      }
+    } else {
+      // ---------------- powers of γ ----------------
+      uint32_t ii = 0;
+      for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x, ++ii) {
+        const LaItem t = la_item(p, item);
+        if (!wait(&pw_empty[ii & 1], ((ii >> 1) & 1) ^ 1)) {
+          give_up(74);
+          break;
+        }
+        const float lg = p.g[t.h] * kLog2e;
+        for (int e = lane; e <= kLaChunk; e += 32) pw_all[(ii & 1) * 132 + e] = la_pow(lg, e);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pw_full[ii & 1]);
+      }
+    }
+  } else if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if (MODE == 0) {
+      // ---------------- scores -> P, outputs ----------------
+      const int wq = warp & 3, row = 32 * wq + lane;
+      const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16);
+      uint32_t it = 0, ii = 0;
+      bool ok = true;
+      for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x, ++ii) {
+        const LaItem t = la_item(p, item);
+        const LaRole& r = *t.r;
+        const int rev = r.rev;
+        const float* pw = pw_all + (ii & 1) * 132;
+        if (!(ok = wait(&pw_full[ii & 1], (ii >> 1) & 1))) break;
+        const float s_intra = r.s_inter * r.s_u;
+        for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
+          const int st = it % NS;
+          const uint32_t ph = it & 1;
+          int64_t t0;
+          const int n = la_chunk(t, i, t0);
+          if (!(ok = wait(sc_full, ph))) break;
+          tc_fence_after();
+          // P's 32 tokens of block blk go to columns 16 blk .., which scores read earlier have left
+#pragma unroll
+          for (int blk = 0; blk < 4; ++blk) {
+            uint32_t w16[16];
+            if (rev ? blk >= wq : blk <= wq) {
+              float f[32];
+              tmem_ld32(tl + kColP + blk * 32, f);
+              const int d0 = rev ? blk * 32 - row : row - blk * 32, sgn = rev ? 1 : -1;  // distance of token j: d0 + sgn j
+              if (blk != wq) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) f[j] *= pw[d0 + sgn * j];
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                  const int d = d0 + sgn * j;
+                  f[j] = d >= 0 ? f[j] * pw[max(d, 0)] : 0.f;
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < 16; ++j) w16[j] = pair(f[2 * j], f[2 * j + 1]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) w16[j] = 0u;
+            }
+            tmem_st16(tl + kColP + blk * 16, w16);
+          }
+          tmem_wait_st();
+          if (!(ok = wait(mx_full, ph))) break;
+          tc_fence_after();
+          float o[DW];
+          const float f_in = r.s_inter * pw[rev ? max(n - 1 - row, 0) : row + 1];
+#pragma unroll
+          for (int k = 0; k < DW / 32; ++k) {
+            float f[32];
+            tmem_ld32(tl + kColO + k * 32, f);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[k * 32 + j] = f_in * f[j];
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_ready);
+          if (!(ok = wait(o_full, ph))) break;
+          tc_fence_after();
+          uint8_t* tile = sm + st * SM::STAGE + SM::W;
+          const bool whole = !r.out_f32 && (n == kLaChunk || t0 + n == p.L);
+          const int64_t at = t.b * r.out_sb + (t0 + row) * r.out_st + (int64_t)t.h * r.dw;
+#pragma unroll
+          for (int k = 0; k < DW / 32; ++k) {
+            float f[32];
+            tmem_ld32(tl + kColO + k * 32, f);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f[j] = fmaf(s_intra, f[j], o[k * 32 + j]);
+            if (whole) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                *reinterpret_cast<uint4*>(tile + (k >> 1) * kTile + swz16(row, (k & 1) * 4 + c)) =
+                    make_uint4(pair(f[8 * c], f[8 * c + 1]), pair(f[8 * c + 2], f[8 * c + 3]),
+                               pair(f[8 * c + 4], f[8 * c + 5]), pair(f[8 * c + 6], f[8 * c + 7]));
+            } else if (row < n) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const int col = k * 32 + 8 * c;
+                if (col >= r.dw) continue;
+                if (r.out_f32) {
+                  float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(r.out) + at + col);
+                  dst[0] = make_float4(f[8 * c], f[8 * c + 1], f[8 * c + 2], f[8 * c + 3]);
+                  dst[1] = make_float4(f[8 * c + 4], f[8 * c + 5], f[8 * c + 6], f[8 * c + 7]);
+                } else {
+                  *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(r.out) + at + col) =
+                      make_uint4(pair(f[8 * c], f[8 * c + 1]), pair(f[8 * c + 2], f[8 * c + 3]),
+                                 pair(f[8 * c + 4], f[8 * c + 5]), pair(f[8 * c + 6], f[8 * c + 7]));
+                }
+              }
+            }
+            __syncwarp();
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(o_free);
+            mbar_arrive(&staged[st]);
+          }
+        }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pw_empty[ii & 1]);
+      }
+      if (!ok) give_up(75);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    // ---------------- the state ----------------
+    const int wq = warp & 3, col = 32 * wq + lane;  // column of M = lane of (γ w)ᵀ and of U
+    const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16);
+    const bool active = col < DW;  // the same for a whole warp
+    if (!active) {  // those rows of (γ w)ᵀ stay zero
+      const uint32_t z[16] = {};
+#pragma unroll
+      for (int k = 0; k < kRing * 3; ++k) tmem_st16(tl + kColRing + k * kPart, z);
+      tmem_wait_st();
+    }
+    uint32_t it = 0, ii = 0;
+    bool ok = true;
+    for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x, ++ii) {
+      const LaItem t = la_item(p, item);
+      const LaRole& r = *t.r;
+      const int rev = r.rev;
+      const float* pw = pw_all + (ii & 1) * 132;
+      const int64_t size = (int64_t)r.dx * r.dw;
+      float m[DX];
+      {
+        const float* start = MODE == 1     ? nullptr
+                             : p.nseg > 1  ? r.seg + (t.bh * p.nseg + t.seg) * size
+                             : r.M0        ? r.M0 + t.bh * size
+                                           : nullptr;
+        const int sj = p.nseg > 1 ? r.dw : r.sj, sc = p.nseg > 1 ? 1 : r.sc;
+#pragma unroll
+        for (int j = 0; j < DX; ++j)
+          m[j] = (start != nullptr && j < r.dx && col < r.dw) ? start[(int64_t)j * sj + (int64_t)col * sc] : 0.f;
+      }
+      if (!(ok = wait(&pw_full[ii & 1], (ii >> 1) & 1))) break;
+      for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
+        const int st = it % NS;
+        int64_t t0;
+        const int n = la_chunk(t, i, t0);
+        if (MODE == 0) {
+          // M's copy; the readout of the chunk before has taken the last one
+          if (it > 0 && !(ok = wait(mx_full, (it & 1) ^ 1))) break;
+          if (active) {
+#pragma unroll
+            for (int c = 0; c < DX / 8; ++c)
+              *reinterpret_cast<uint4*>(sm + SM::M + (c >> 3) * (DW * 128) + swz16(col, c & 7)) =
+                  make_uint4(pair(m[8 * c], m[8 * c + 1]), pair(m[8 * c + 2], m[8 * c + 3]),
+                             pair(m[8 * c + 4], m[8 * c + 5]), pair(m[8 * c + 6], m[8 * c + 7]));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(m_ready);
+        }
+        if (!(ok = wait(&full[st], (it / NS) & 1))) break;
+        const uint8_t* tw = sm + st * SM::STAGE + SM::W + (col >> 6) * kTile + (col & 7) * 2;
+        const int w0 = rev ? 1 : n - 1, wd = rev ? 1 : -1;  // token s enters M with γ^(w0 + wd s)
+        for (int qr = 0; qr < 4; ++qr) {
+          const uint32_t slot = qr & 1, use = it * 2 + (qr >> 1);
+          if (!(ok = wait(&ring_empty[slot], (use & 1) ^ 1))) break;
+          tc_fence_after();
+          if (active) {
+            uint32_t hi[16], mid[16], lo[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float v[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int s = 32 * qr + 2 * j + e;
+                const uint32_t raw = *reinterpret_cast<const uint16_t*>(tw + s * 128 + ((((col & 63) >> 3) ^ (s & 7)) << 4));
+                v[e] = s < n ? __uint_as_float(raw << 16) * pw[max(w0 + wd * s, 0)] : 0.f;
+              }
+              hi[j] = pair(v[0], v[1]);
+              v[0] -= bf16lo(hi[j]);
+              v[1] -= bf16hi(hi[j]);
+              mid[j] = pair(v[0], v[1]);
+              lo[j] = pair(v[0] - bf16lo(mid[j]), v[1] - bf16hi(mid[j]));
+            }
+            const uint32_t at = tl + kColRing + slot * 3 * kPart;
+            tmem_st16(at, hi);
+            tmem_st16(at + kPart, mid);
+            tmem_st16(at + 2 * kPart, lo);
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ring_full[slot]);
+        }
+        if (!ok) break;
+        if (!(ok = wait(u_full, it & 1))) break;
+        tc_fence_after();
+        if (active) {
+          const float g = pw[n];
+#pragma unroll
+          for (int k = 0; k < DX / 32; ++k) {
+            float f[32];
+            tmem_ld32(tl + kColU + k * 32, f);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) m[k * 32 + j] = fmaf(g, m[k * 32 + j], r.s_u * f[j]);
+          }
+        }
+        tc_fence_before();
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pw_empty[ii & 1]);
+      if (col < r.dw && (MODE == 1 || (p.nseg == 1 && r.M_end != nullptr))) {
+        float* end = MODE == 1 ? r.seg + (t.bh * p.nseg + t.seg) * size : r.M_end + t.bh * size;
+        const int ej = MODE == 1 ? r.dw : r.sj, ec = MODE == 1 ? 1 : r.sc;
+#pragma unroll
+        for (int j = 0; j < DX; ++j)
+          if (j < r.dx) end[(int64_t)j * ej + (int64_t)col * ec] = m[j];
+      }
+    }
+    if (!ok) give_up(76);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---- host -----------------------------------------------------------------------------------------------
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 la_encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return (PFN_cuTensorMapEncodeTiled_v12000) nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// [B, L, heads, d] bf16 with token stride st: boxes of 128 tokens x 64 channels of one head; what lies
+// behind d or L reads as zeros and is not written.
+bool la_map(CUtensorMap* m, const void* base, int d, int heads, int64_t st, int64_t L, int64_t B) {
+  auto fn = la_encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)L, (cuuint64_t)B};
+  cuuint64_t str[3] = {(cuuint64_t)(d * 2), (cuuint64_t)(st * 2), (cuuint64_t)(st * L * 2)};
+  cuuint32_t box[4] = {64, 1, (cuuint32_t)kLaChunk, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, str, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DX, int DW, int MODE>
+cudaError_t launch_tc(const LaTcArgs& a, int sms, cudaStream_t s) {
+  constexpr int smem = 1024 + LaSmem<DX, DW, MODE>::BYTES;
+  const cudaError_t e = cudaFuncSetAttribute(la_tc_kernel<DX, DW, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  la_tc_kernel<DX, DW, MODE><<<(unsigned)std::min<int64_t>(a.items, sms), kThreads, smem, s>>>(a);
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// One launch over roles of the same padded sizes. states: only the segments' end states.
+cudaError_t run_la_tc(const LaParams& p, bool states, cudaStream_t s) {
+  LaTcArgs a;
+  a.p = p;
+  a.items = (int64_t)p.n_roles * p.B * p.H * p.nseg;
+  for (int i = 0; i < p.n_roles; ++i) {
+    const LaRole& r = p.role[i];
+    if (!la_map(&a.map[i][kMapX], r.x.p, r.dx, p.H / r.x.div, r.x.st, p.L, p.B) ||
+        !la_map(&a.map[i][kMapY], r.y.p, r.dx, p.H / r.y.div, r.y.st, p.L, p.B) ||
+        !la_map(&a.map[i][kMapW], r.w.p, r.dw, p.H / r.w.div, r.w.st, p.L, p.B) ||
+        (!r.out_f32 && !la_map(&a.map[i][kMapOut], r.out, r.dw, p.H, r.out_st, p.L, p.B)))
+      return cudaErrorInvalidValue;
+  }
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const bool x64 = p.role[0].dx <= 64, w64 = p.role[0].dw <= 64;
+  if (states)
+    return x64 ? (w64 ? launch_tc<64, 64, 1>(a, sms, s) : launch_tc<64, 128, 1>(a, sms, s))
+               : (w64 ? launch_tc<128, 64, 1>(a, sms, s) : launch_tc<128, 128, 1>(a, sms, s));
+  return x64 ? (w64 ? launch_tc<64, 64, 0>(a, sms, s) : launch_tc<64, 128, 0>(a, sms, s))
+             : (w64 ? launch_tc<128, 64, 0>(a, sms, s) : launch_tc<128, 128, 0>(a, sms, s));
+}
+
+}  // namespace swimba
