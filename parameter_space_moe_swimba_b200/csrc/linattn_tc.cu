@@ -42,6 +42,8 @@ constexpr int kThreads = 384;
 constexpr int kRing = 2, kPart = 16;   // γ w ring: 2 quarters x 3 parts x 16 columns
 constexpr uint32_t kColP = 0, kColO = 128, kColU = 256, kColRing = 384;
 
+constexpr int kTable = 32 + kLaChunk;  // per item: γ^(31-j) (reverse: γ^j) of a block's 32 columns; γ^(127-s) (γ^(s+1))
+
 enum { kMapX, kMapY, kMapW, kMapOut };
 
 struct LaTcArgs {
@@ -59,8 +61,8 @@ struct LaSmem {
   static constexpr int ROOM = 229376 - COPY;
   static constexpr int NS = ROOM / STAGE < 4 ? ROOM / STAGE : 4;
   static constexpr int M = NS * STAGE;
-  static constexpr int POW = M + COPY;              // 2 x 132 floats
-  static constexpr int BAR = POW + 2 * 132 * 4;     // barriers
+  static constexpr int POW = M + COPY;              // 2 x kTable floats
+  static constexpr int BAR = POW + 2 * kTable * 4;  // barriers
   static constexpr int NBAR = 3 * NS + 6 + 2 * kRing + 1 + 4 + 1;
   static constexpr int MISC = BAR + NBAR * 8;
   static constexpr int BYTES = MISC + 16;
@@ -73,6 +75,36 @@ __device__ __forceinline__ uint32_t swz16(int r, int c) { return (uint32_t)(r * 
 __device__ __forceinline__ uint32_t pair(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Shared memory through its own address space: pointers cut from the aligned base are generic to the
+// compiler, and generic accesses cost a chunk several times its arithmetic (8.0 against 0.6 thousand
+// cycles for P's 128 x 128 factors).
+__device__ __forceinline__ float4 lds4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ float2 lds2(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void sts4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// Four 8 x 8 matrices of bf16, transposed: thread t gets of matrix k the elements (2 (t % 4) + 0..1, t / 4)
+// of the stored one, whose row i starts at the address that thread 8 k + i gives.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at));
+}
+// 16 lanes x 16 columns: thread t's r[2 k] is lane t / 4, r[2 k + 1] lane t / 4 + 8, column 4 k + t % 4.
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 struct LaItem {
@@ -111,7 +143,6 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
   constexpr int NS = SM::NS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* pw_all = reinterpret_cast<float*>(sm + SM::POW);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + SM::BAR);  // [NS] tiles landed
   uint64_t* empty = full + NS;                                 // [NS] stage free
   uint64_t* staged = empty + NS;                               // [NS] output tile written
@@ -166,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
   const uint32_t tmem = *tmem_slot;
   // The whole warp waits and goes on, or gives up, together.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+    return __all_sync(0xffffffffu, mbar_wait_close(bar, parity, abort_flag));
   };
   auto give_up = [&](int where) {
     *abort_flag = 1;
@@ -345,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         __syncwarp();
       }
     } else {
-      // ---------------- powers of γ ----------------
+      // ---------------- an item's powers of γ ----------------
       uint32_t ii = 0;
       for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x, ++ii) {
         const LaItem t = la_item(p, item);
@@ -354,7 +385,10 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           break;
         }
         const float lg = p.g[t.h] * kLog2e;
-        for (int e = lane; e <= kLaChunk; e += 32) pw_all[(ii & 1) * 132 + e] = la_pow(lg, e);
+        const int rev = t.r->rev;
+        float* table = reinterpret_cast<float*>(sm + SM::POW) + (ii & 1) * kTable;
+        table[lane] = la_pow(lg, rev ? lane : 31 - lane);
+        for (int e = lane; e < kLaChunk; e += 32) table[32 + e] = la_pow(lg, rev ? e + 1 : kLaChunk - 1 - e);
         __syncwarp();
         if (lane == 0) mbar_arrive(&pw_full[ii & 1]);
       }
@@ -371,7 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         const LaItem t = la_item(p, item);
         const LaRole& r = *t.r;
         const int rev = r.rev;
-        const float* pw = pw_all + (ii & 1) * 132;
+        const uint32_t table = smem_u32(sm) + SM::POW + (ii & 1) * kTable * 4;
+        const float lg = p.g[t.h] * kLog2e;
         if (!(ok = wait(&pw_full[ii & 1], (ii >> 1) & 1))) break;
         const float s_intra = r.s_inter * r.s_u;
         for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
@@ -381,22 +416,30 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           const int n = la_chunk(t, i, t0);
           if (!(ok = wait(sc_full, ph))) break;
           tc_fence_after();
-          // P's 32 tokens of block blk go to columns 16 blk .., which scores read earlier have left
-#pragma unroll
+          // P's 32 tokens of block blk go to columns 16 blk .., which scores read earlier have left. A block
+          // on one side of the diagonal takes γ^distance as the row's power to the block's nearest column
+          // times the column's from there (both <= 1), the diagonal's own takes it whole.
+#pragma unroll 1
           for (int blk = 0; blk < 4; ++blk) {
             uint32_t w16[16];
             if (rev ? blk >= wq : blk <= wq) {
               float f[32];
               tmem_ld32(tl + kColP + blk * 32, f);
-              const int d0 = rev ? blk * 32 - row : row - blk * 32, sgn = rev ? 1 : -1;  // distance of token j: d0 + sgn j
               if (blk != wq) {
+                const float rp = la_pow(lg, rev ? blk * 32 - row : row - blk * 32 - 31);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) f[j] *= pw[d0 + sgn * j];
+                for (int j = 0; j < 32; j += 4) {
+                  const float4 c = lds4(table + j * 4);
+                  f[j] *= rp * c.x;
+                  f[j + 1] *= rp * c.y;
+                  f[j + 2] *= rp * c.z;
+                  f[j + 3] *= rp * c.w;
+                }
               } else {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                  const int d = d0 + sgn * j;
-                  f[j] = d >= 0 ? f[j] * pw[max(d, 0)] : 0.f;
+                  const int d = rev ? j - lane : lane - j;
+                  f[j] = d > 0 ? f[j] * ex2_approx(lg * (float)d) : d == 0 ? f[j] : 0.f;
                 }
               }
 #pragma unroll
@@ -411,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           if (!(ok = wait(mx_full, ph))) break;
           tc_fence_after();
           float o[DW];
-          const float f_in = r.s_inter * pw[rev ? max(n - 1 - row, 0) : row + 1];
+          const float f_in = r.s_inter * la_pow(lg, rev ? max(n - 1 - row, 0) : row + 1);
 #pragma unroll
           for (int k = 0; k < DW / 32; ++k) {
             float f[32];
@@ -424,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           if (lane == 0) mbar_arrive(p_ready);
           if (!(ok = wait(o_full, ph))) break;
           tc_fence_after();
-          uint8_t* tile = sm + st * SM::STAGE + SM::W;
+          const uint32_t tile = smem_u32(sm) + st * SM::STAGE + SM::W;
           const bool whole = !r.out_f32 && (n == kLaChunk || t0 + n == p.L);
           const int64_t at = t.b * r.out_sb + (t0 + row) * r.out_st + (int64_t)t.h * r.dw;
 #pragma unroll
@@ -436,9 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             if (whole) {
 #pragma unroll
               for (int c = 0; c < 4; ++c)
-                *reinterpret_cast<uint4*>(tile + (k >> 1) * kTile + swz16(row, (k & 1) * 4 + c)) =
-                    make_uint4(pair(f[8 * c], f[8 * c + 1]), pair(f[8 * c + 2], f[8 * c + 3]),
-                               pair(f[8 * c + 4], f[8 * c + 5]), pair(f[8 * c + 6], f[8 * c + 7]));
+                sts4(tile + (k >> 1) * kTile + swz16(row, (k & 1) * 4 + c), pair(f[8 * c], f[8 * c + 1]),
+                     pair(f[8 * c + 2], f[8 * c + 3]), pair(f[8 * c + 4], f[8 * c + 5]), pair(f[8 * c + 6], f[8 * c + 7]));
             } else if (row < n) {
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
@@ -489,7 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       const LaItem t = la_item(p, item);
       const LaRole& r = *t.r;
       const int rev = r.rev;
-      const float* pw = pw_all + (ii & 1) * 132;
+      const uint32_t table = smem_u32(sm) + SM::POW + (ii & 1) * kTable * 4 + 128;
+      const float lg = p.g[t.h] * kLog2e;
       const int64_t size = (int64_t)r.dx * r.dw;
       float m[DX];
       {
@@ -513,42 +556,59 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           if (active) {
 #pragma unroll
             for (int c = 0; c < DX / 8; ++c)
-              *reinterpret_cast<uint4*>(sm + SM::M + (c >> 3) * (DW * 128) + swz16(col, c & 7)) =
-                  make_uint4(pair(m[8 * c], m[8 * c + 1]), pair(m[8 * c + 2], m[8 * c + 3]),
-                             pair(m[8 * c + 4], m[8 * c + 5]), pair(m[8 * c + 6], m[8 * c + 7]));
+              sts4(smem_u32(sm) + SM::M + (c >> 3) * (DW * 128) + swz16(col, c & 7), pair(m[8 * c], m[8 * c + 1]),
+                   pair(m[8 * c + 2], m[8 * c + 3]), pair(m[8 * c + 4], m[8 * c + 5]), pair(m[8 * c + 6], m[8 * c + 7]));
           }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(m_ready);
         }
         if (!(ok = wait(&full[st], (it / NS) & 1))) break;
-        const uint8_t* tw = sm + st * SM::STAGE + SM::W + (col >> 6) * kTile + (col & 7) * 2;
-        const int w0 = rev ? 1 : n - 1, wd = rev ? 1 : -1;  // token s enters M with γ^(w0 + wd s)
+        // (γ w)ᵀ, 32 tokens at a time: 8 x 8 blocks of W transposed on the way to the registers, where
+        // thread t holds channel t / 4 of tokens 2 (t % 4) + 0..1, scaled, split and stored in that form
+        const uint32_t tw = smem_u32(sm) + st * SM::STAGE + SM::W + (wq >> 1) * kTile + (lane & 7) * 128;
+#pragma unroll 1
         for (int qr = 0; qr < 4; ++qr) {
           const uint32_t slot = qr & 1, use = it * 2 + (qr >> 1);
           if (!(ok = wait(&ring_empty[slot], (use & 1) ^ 1))) break;
           tc_fence_after();
           if (active) {
-            uint32_t hi[16], mid[16], lo[16];
+            float2 wt[4];
+            uint32_t keep[4];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              float v[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int s = 32 * qr + 2 * j + e;
-                const uint32_t raw = *reinterpret_cast<const uint16_t*>(tw + s * 128 + ((((col & 63) >> 3) ^ (s & 7)) << 4));
-                v[e] = s < n ? __uint_as_float(raw << 16) * pw[max(w0 + wd * s, 0)] : 0.f;
+            for (int g = 0; g < 4; ++g) {
+              const int s = 32 * qr + 8 * g + 2 * (lane & 3);
+              wt[g] = lds2(table + s * 4);
+              keep[g] = 0xffffffffu;
+              if (n < kLaChunk) {  // the last chunk's decays count from its last token; behind it nothing is read
+                if (!rev) wt[g] = make_float2(la_pow(lg, max(n - 1 - s, 0)), la_pow(lg, max(n - 2 - s, 0)));
+                keep[g] = (s < n ? 0xffffu : 0u) | (s + 1 < n ? 0xffff0000u : 0u);
               }
-              hi[j] = pair(v[0], v[1]);
-              v[0] -= bf16lo(hi[j]);
-              v[1] -= bf16hi(hi[j]);
-              mid[j] = pair(v[0], v[1]);
-              lo[j] = pair(v[0] - bf16lo(mid[j]), v[1] - bf16hi(mid[j]));
             }
-            const uint32_t at = tl + kColRing + slot * 3 * kPart;
-            tmem_st16(at, hi);
-            tmem_st16(at + kPart, mid);
-            tmem_st16(at + 2 * kPart, lo);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t hi[8], mid[8], lo[8];
+#pragma unroll
+              for (int g2 = 0; g2 < 2; ++g2) {  // matrices (8 tokens, 8 channels): (0, 0), (0, 1), (1, 0), (1, 1)
+                uint32_t raw[4];
+                const int chunk = ((wq & 1) * 4 + half * 2 + ((lane >> 3) & 1)) ^ (lane & 7);
+                ldmatrix_x4_trans(tw + (32 * qr + 16 * g2 + 8 * (lane >> 4)) * 128 + (chunk << 4), raw);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int g = 2 * g2 + (k >> 1), d = 4 * g2 + k;
+                  const uint32_t v = raw[k] & keep[g];
+                  const float v0 = bf16lo(v) * wt[g].x, v1 = bf16hi(v) * wt[g].y;
+                  hi[d] = pair(v0, v1);
+                  const float r0 = v0 - bf16lo(hi[d]), r1 = v1 - bf16hi(hi[d]);
+                  mid[d] = pair(r0, r1);
+                  lo[d] = pair(r0 - bf16lo(mid[d]), r1 - bf16hi(mid[d]));
+                }
+              }
+              const uint32_t at = tl + ((uint32_t)(16 * half) << 16) + kColRing + slot * 3 * kPart;
+              tmem_st_16x128b_x4(at, hi);
+              tmem_st_16x128b_x4(at + kPart, mid);
+              tmem_st_16x128b_x4(at + 2 * kPart, lo);
+            }
             tmem_wait_st();
           }
           tc_fence_before();
@@ -559,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         if (!(ok = wait(u_full, it & 1))) break;
         tc_fence_after();
         if (active) {
-          const float g = pw[n];
+          const float g = la_pow(lg, n);
 #pragma unroll
           for (int k = 0; k < DX / 32; ++k) {
             float f[32];
