@@ -16,8 +16,8 @@
 //                carried state's readout into registers, the sum of both into the W tile, which no
 //                MMA reads any more, and from there to memory
 //   warps 8-11   one column c of M each, in fp32 registers for the whole item: M's bf16 copy for the
-//                readout (the only rounding of M), (γ w)ᵀ as three bf16 parts into tensor memory (a
-//                ring of two 32-token quarters), M <- γ^n M + U
+//                readout (the only rounding of M), M <- γ^n M + U
+//   warps 12-15  (γ w)ᵀ as three bf16 parts into tensor memory (a ring of two 32-token quarters)
 // Rounded to bf16: P and M's copy, once each, because each meets a bf16 operand and makes a bf16
 // output; γ w enters M as hi + mid + lo, 24 bits together, so that M stays an fp32 state (two parts
 // would put 3e-6 into S_final and dS0, three 1e-7).
@@ -38,7 +38,7 @@ using namespace sm100;
 namespace {
 
 constexpr int kTile = kLaChunk * 128;  // 128 tokens x 128 bytes (64 bf16), 128-byte swizzle: 16 KB
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kRing = 2, kPart = 16;   // γ w ring: 2 quarters x 3 parts x 16 columns
 constexpr uint32_t kColP = 0, kColO = 128, kColU = 256, kColRing = 384;
 
@@ -63,7 +63,7 @@ struct LaSmem {
   static constexpr int M = NS * STAGE;
   static constexpr int POW = M + COPY;              // 2 x kTable floats
   static constexpr int BAR = POW + 2 * kTable * 4;  // barriers
-  static constexpr int NBAR = 3 * NS + 6 + 2 * kRing + 1 + 4 + 1;
+  static constexpr int NBAR = 3 * NS + 6 + 2 * kRing + 2 + 4 + 1;
   static constexpr int MISC = BAR + NBAR * 8;
   static constexpr int BYTES = MISC + 16;
   static_assert(NS >= 2, "two stages");
@@ -106,6 +106,12 @@ __device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
+
+// The upper 16 bits of a float (a bf16, truncated), of two packed, and as a float.
+__device__ __forceinline__ uint32_t high_halves(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ float top_bits(float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); }
 
 struct LaItem {
   const LaRole* r;
@@ -155,7 +161,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
   uint64_t* ring_full = o_free + 1;                            // [kRing]
   uint64_t* ring_empty = ring_full + kRing;                    // [kRing]
   uint64_t* u_full = ring_empty + kRing;
-  uint64_t* pw_full = u_full + 1;                              // [2]
+  uint64_t* u_free = u_full + 1;                               // U read
+  uint64_t* pw_full = u_free + 1;                              // [2]
   uint64_t* pw_empty = pw_full + 2;                            // [2]
   uint64_t* done = pw_empty + 2;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + SM::MISC);
@@ -180,9 +187,10 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       mbar_init(&ring_empty[i], 1);
     }
     mbar_init(u_full, 1);
+    mbar_init(u_free, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&pw_full[i], 1);
-      mbar_init(&pw_empty[i], MODE == 0 ? 8 : 4);
+      mbar_init(&pw_empty[i], MODE == 0 ? 8 : 4);  // warps 4-7 (MODE 0) and 12-15
     }
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -205,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
   };
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp == 0) {
       // ---------------- loads ----------------
       uint32_t it = 0;
@@ -221,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             ok = false;
             break;
           }
-          if (lane == 0) {
+          if (elect_one()) {
             uint8_t* s = sm + st * SM::STAGE;
             mbar_arrive_expect_tx(&full[st], SM::STAGE);
 #pragma unroll
@@ -249,7 +257,11 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       // ---------------- MMAs ----------------
       constexpr uint32_t id_sc = idesc_bf16(128, 128, false), id_mx = idesc_bf16(128, DW, false),
                          id_u = idesc_bf16(128, DX, true), id_pw = idesc_bf16(128, DW, true);
-      const uint32_t base = smem_u32(sm), sM = base + SM::M;
+      const uint32_t base = smem_u32(sm);
+      // descriptors of address 0, to which a tile's address / 16 is added; the loops stay rolled, so that
+      // the issuing warp's few instructions stay in the instruction cache beside the other warps'
+      const uint64_t dK = smem_desc(0, 16, 1024, kLayoutSW128), dMN = smem_desc(0, kTile, 1024, kLayoutSW128);
+      auto kstep = [](int ks, int box) { return (uint32_t)((ks >> 2) * (box >> 4) + (ks & 3) * 2); };
       uint32_t it = 0;
       bool ok = true;
       for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
@@ -259,8 +271,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           const uint32_t ph = it & 1;
           int64_t t0;
           const int n = la_chunk(t, i, t0);
-          const uint32_t sX = base + st * SM::STAGE + SM::X, sY = base + st * SM::STAGE + SM::Y,
-                         sW = base + st * SM::STAGE + SM::W;
+          const uint32_t sX = (base + st * SM::STAGE + SM::X) >> 4, sY = (base + st * SM::STAGE + SM::Y) >> 4,
+                         sW = (base + st * SM::STAGE + SM::W) >> 4;
           if (!(ok = wait(&full[st], (it / NS) & 1))) break;
           if (n < kLaChunk && t0 + n < p.L) {
             // tokens behind the sequence's end that lie in memory: whatever they hold, they are zeros here
@@ -277,13 +289,10 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             // scores; P of the chunk before has been read
             if (it > 0 && !(ok = wait(o_full, ph ^ 1))) break;
             tc_fence_after();
-            if (lane == 0) {
-#pragma unroll
-              for (int ks = 0; ks < DX / 16; ++ks) {
-                const uint32_t off = (ks >> 2) * kTile + (ks & 3) * 32;
-                mma_bf16(tmem + kColP, smem_desc(sX + off, 16, 1024, kLayoutSW128),
-                         smem_desc(sY + off, 16, 1024, kLayoutSW128), id_sc, ks > 0);
-              }
+            if (elect_one()) {
+#pragma unroll 1
+              for (int ks = 0; ks < DX / 16; ++ks)
+                mma_bf16(tmem + kColP, dK + sX + kstep(ks, kTile), dK + sY + kstep(ks, kTile), id_sc, ks > 0);
               mma_commit(sc_full);
             }
             __syncwarp();
@@ -291,34 +300,33 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             if (!(ok = wait(m_ready, ph))) break;
             if (it > 0 && !(ok = wait(o_free, ph ^ 1))) break;
             tc_fence_after();
-            if (lane == 0) {
-#pragma unroll
+            if (elect_one()) {
+#pragma unroll 1
               for (int ks = 0; ks < DX / 16; ++ks)
-                mma_bf16(tmem + kColO, smem_desc(sX + (ks >> 2) * kTile + (ks & 3) * 32, 16, 1024, kLayoutSW128),
-                         smem_desc(sM + (ks >> 2) * (DW * 128) + (ks & 3) * 32, 16, 1024, kLayoutSW128), id_mx, ks > 0);
+                mma_bf16(tmem + kColO, dK + sX + kstep(ks, kTile), dK + ((base + SM::M) >> 4) + kstep(ks, DW * 128), id_mx,
+                         ks > 0);
               mma_commit(mx_full);
             }
             __syncwarp();
           }
           // U = Σ_s (γ w_s) y_sᵀ, 32 tokens at a time
+          if (it > 0 && !(ok = wait(u_free, ph ^ 1))) break;
+#pragma unroll 1
           for (int qr = 0; qr < 4; ++qr) {
             const uint32_t slot = qr & 1, use = it * 2 + (qr >> 1);
             if (!(ok = wait(&ring_full[slot], use & 1))) break;
             tc_fence_after();
-            if (lane == 0) {
-#pragma unroll
-              for (int part = 0; part < 3; ++part)
-#pragma unroll
-                for (int k2 = 0; k2 < 2; ++k2)
-                  mma_bf16_ts(tmem + kColU, tmem + kColRing + slot * 3 * kPart + part * kPart + k2 * 8,
-                              smem_desc(sY + (qr * 32 + k2 * 16) * 128, kTile, 1024, kLayoutSW128), id_u,
-                              (qr | part | k2) != 0);
+            if (elect_one()) {
+#pragma unroll 1
+              for (int k = 0; k < 6; ++k)  // part k / 2, tokens 16 (k % 2) ..
+                mma_bf16_ts(tmem + kColU, tmem + kColRing + slot * 3 * kPart + k * 8, dMN + sY + (qr * 2 + (k & 1)) * 128, id_u,
+                            (qr | k) != 0);
               mma_commit(&ring_empty[slot]);
             }
             __syncwarp();
           }
           if (!ok) break;
-          if (lane == 0) {
+          if (elect_one()) {
             mma_commit(u_full);
             if (MODE == 1) mma_commit(&empty[st]);
           }
@@ -326,11 +334,10 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           if (MODE == 0) {
             if (!(ok = wait(p_ready, ph))) break;
             tc_fence_after();
-            if (lane == 0) {
-#pragma unroll
+            if (elect_one()) {
+#pragma unroll 1
               for (int ks = 0; ks < kLaChunk / 16; ++ks)
-                mma_bf16_ts(tmem + kColO, tmem + kColP + ks * 8, smem_desc(sW + ks * 16 * 128, kTile, 1024, kLayoutSW128),
-                            id_pw, ks > 0);
+                mma_bf16_ts(tmem + kColO, tmem + kColP + ks * 8, dMN + sW + ks * 128, id_pw, ks > 0);
               mma_commit(o_full);
             }
             __syncwarp();
@@ -339,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       }
       if (!ok) give_up(72);
       // every MMA of the CTA has completed when `done` does
-      if (lane == 0) {
+      if (elect_one()) {
         mma_commit(done);
         const uint64_t w0 = globaltimer_ns();
         while (!mbar_try_wait(done, 0) && globaltimer_ns() - w0 < kWaitLimitNs) {
@@ -358,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             int64_t t0;
             const int n = la_chunk(t, i, t0);
             if (!(ok = wait(&staged[st], (it / NS) & 1))) break;
-            if (lane == 0) {
+            if (elect_one()) {
               if (!t.r->out_f32 && (n == kLaChunk || t0 + n == p.L)) {
 #pragma unroll
                 for (int k = 0; k < SM::WB; ++k)
@@ -372,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           }
         }
         if (!ok) give_up(73);
-        if (lane == 0) bulk_wait<0>();
+        if (elect_one()) bulk_wait<0>();
         __syncwarp();
       }
     } else {
@@ -394,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       }
     }
   } else if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     if (MODE == 0) {
       // ---------------- scores -> P, outputs ----------------
       const int wq = warp & 3, row = 32 * wq + lane;
@@ -513,26 +520,18 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       }
       if (!ok) give_up(75);
     }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     // ---------------- the state ----------------
-    const int wq = warp & 3, col = 32 * wq + lane;  // column of M = lane of (γ w)ᵀ and of U
+    const int wq = warp & 3, col = 32 * wq + lane;  // column of M = lane of U
     const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16);
     const bool active = col < DW;  // the same for a whole warp
-    if (!active) {  // those rows of (γ w)ᵀ stay zero
-      const uint32_t z[16] = {};
-#pragma unroll
-      for (int k = 0; k < kRing * 3; ++k) tmem_st16(tl + kColRing + k * kPart, z);
-      tmem_wait_st();
-    }
-    uint32_t it = 0, ii = 0;
+    uint32_t it = 0;
     bool ok = true;
-    for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x, ++ii) {
+    for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
       const LaItem t = la_item(p, item);
       const LaRole& r = *t.r;
-      const int rev = r.rev;
-      const uint32_t table = smem_u32(sm) + SM::POW + (ii & 1) * kTable * 4 + 128;
-      const float lg = p.g[t.h] * kLog2e;
+      const float lg = p.g[t.h] * kLog2e, g_all = la_pow(lg, kLaChunk);
       const int64_t size = (int64_t)r.dx * r.dw;
       float m[DX];
       {
@@ -545,9 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         for (int j = 0; j < DX; ++j)
           m[j] = (start != nullptr && j < r.dx && col < r.dw) ? start[(int64_t)j * sj + (int64_t)col * sc] : 0.f;
       }
-      if (!(ok = wait(&pw_full[ii & 1], (ii >> 1) & 1))) break;
       for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
-        const int st = it % NS;
         int64_t t0;
         const int n = la_chunk(t, i, t0);
         if (MODE == 0) {
@@ -563,9 +560,59 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           __syncwarp();
           if (lane == 0) mbar_arrive(m_ready);
         }
+        if (!(ok = wait(u_full, it & 1))) break;
+        tc_fence_after();
+        if (active) {
+          const float g = n == kLaChunk ? g_all : la_pow(lg, n);
+#pragma unroll
+          for (int k = 0; k < DX / 32; ++k) {
+            float f[32];
+            tmem_ld32(tl + kColU + k * 32, f);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) m[k * 32 + j] = fmaf(g, m[k * 32 + j], r.s_u * f[j]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(u_free);
+      }
+      if (!ok) break;
+      if (col < r.dw && (MODE == 1 || (p.nseg == 1 && r.M_end != nullptr))) {
+        float* end = MODE == 1 ? r.seg + (t.bh * p.nseg + t.seg) * size : r.M_end + t.bh * size;
+        const int ej = MODE == 1 ? r.dw : r.sj, ec = MODE == 1 ? 1 : r.sc;
+#pragma unroll
+        for (int j = 0; j < DX; ++j)
+          if (j < r.dx) end[(int64_t)j * ej + (int64_t)col * ec] = m[j];
+      }
+    }
+    if (!ok) give_up(76);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    // ---------------- (γ w)ᵀ ----------------
+    const int wq = warp & 3;
+    const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16);
+    const bool active = 32 * wq < DW;
+    if (!active) {  // those rows stay zero
+      const uint32_t z[16] = {};
+#pragma unroll
+      for (int k = 0; k < kRing * 3; ++k) tmem_st16(tl + kColRing + k * kPart, z);
+      tmem_wait_st();
+    }
+    uint32_t it = 0, ii = 0;
+    bool ok = true;
+    for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x, ++ii) {
+      const LaItem t = la_item(p, item);
+      const int rev = t.r->rev;
+      const uint32_t table = smem_u32(sm) + SM::POW + (ii & 1) * kTable * 4 + 128;
+      const float lg = p.g[t.h] * kLog2e;
+      if (!(ok = wait(&pw_full[ii & 1], (ii >> 1) & 1))) break;
+      for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
+        const int st = it % NS;
+        int64_t t0;
+        const int n = la_chunk(t, i, t0);
         if (!(ok = wait(&full[st], (it / NS) & 1))) break;
-        // (γ w)ᵀ, 32 tokens at a time: 8 x 8 blocks of W transposed on the way to the registers, where
-        // thread t holds channel t / 4 of tokens 2 (t % 4) + 0..1, scaled, split and stored in that form
+        // 32 tokens at a time: 8 x 8 blocks of W, transposed on the way to the registers, where thread t
+        // holds channel t / 4 of tokens 2 (t % 4) + 0..1, scaled, split and stored in that form
         const uint32_t tw = smem_u32(sm) + st * SM::STAGE + SM::W + (wq >> 1) * kTile + (lane & 7) * 128;
 #pragma unroll 1
         for (int qr = 0; qr < 4; ++qr) {
@@ -585,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                 keep[g] = (s < n ? 0xffffu : 0u) | (s + 1 < n ? 0xffff0000u : 0u);
               }
             }
-#pragma unroll
+#pragma unroll 1
             for (int half = 0; half < 2; ++half) {
               uint32_t hi[8], mid[8], lo[8];
 #pragma unroll
@@ -595,13 +642,14 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                 ldmatrix_x4_trans(tw + (32 * qr + 16 * g2 + 8 * (lane >> 4)) * 128 + (chunk << 4), raw);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
+                  // three truncated parts of 8 bits each: their sum is the product's 24 bits
                   const int g = 2 * g2 + (k >> 1), d = 4 * g2 + k;
                   const uint32_t v = raw[k] & keep[g];
                   const float v0 = bf16lo(v) * wt[g].x, v1 = bf16hi(v) * wt[g].y;
-                  hi[d] = pair(v0, v1);
-                  const float r0 = v0 - bf16lo(hi[d]), r1 = v1 - bf16hi(hi[d]);
-                  mid[d] = pair(r0, r1);
-                  lo[d] = pair(r0 - bf16lo(mid[d]), r1 - bf16hi(mid[d]));
+                  hi[d] = high_halves(v0, v1);
+                  const float r0 = v0 - top_bits(v0), r1 = v1 - top_bits(v1);
+                  mid[d] = high_halves(r0, r1);
+                  lo[d] = high_halves(r0 - top_bits(r0), r1 - top_bits(r1));
                 }
               }
               const uint32_t at = tl + ((uint32_t)(16 * half) << 16) + kColRing + slot * 3 * kPart;
@@ -616,32 +664,12 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           if (lane == 0) mbar_arrive(&ring_full[slot]);
         }
         if (!ok) break;
-        if (!(ok = wait(u_full, it & 1))) break;
-        tc_fence_after();
-        if (active) {
-          const float g = la_pow(lg, n);
-#pragma unroll
-          for (int k = 0; k < DX / 32; ++k) {
-            float f[32];
-            tmem_ld32(tl + kColU + k * 32, f);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) m[k * 32 + j] = fmaf(g, m[k * 32 + j], r.s_u * f[j]);
-          }
-        }
-        tc_fence_before();
       }
       if (!ok) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&pw_empty[ii & 1]);
-      if (col < r.dw && (MODE == 1 || (p.nseg == 1 && r.M_end != nullptr))) {
-        float* end = MODE == 1 ? r.seg + (t.bh * p.nseg + t.seg) * size : r.M_end + t.bh * size;
-        const int ej = MODE == 1 ? r.dw : r.sj, ec = MODE == 1 ? 1 : r.sc;
-#pragma unroll
-        for (int j = 0; j < DX; ++j)
-          if (j < r.dx) end[(int64_t)j * ej + (int64_t)col * ec] = m[j];
-      }
     }
-    if (!ok) give_up(76);
+    if (!ok) give_up(77);
   }
   tc_fence_before();
   __syncthreads();
