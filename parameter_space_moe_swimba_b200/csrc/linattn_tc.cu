@@ -12,12 +12,15 @@
 //   warp 1       issues every MMA
 //   warp 2       TMA stores of the finished output tiles
 //   warp 3       the head's table of powers γ^0 .. γ^128
-//   warps 4-7    one row i = TMEM lane each: scores -> P (bf16, in place, the A operand of P W), the
-//                carried state's readout into registers, the sum of both into the W tile, which no
-//                MMA reads any more, and from there to memory
-//   warps 8-11   one column c of M each, in fp32 registers for the whole item: M's bf16 copy for the
-//                readout (the only rounding of M), M <- γ^n M + U
-//   warps 12-15  (γ w)ᵀ as three bf16 parts into tensor memory (a ring of two 32-token quarters)
+//   warps 4-7    scores -> P: bf16, in place, the A operand of P W; one row i = TMEM lane each
+//   warps 8-11   the outputs' rows: the carried state's readout scaled in place, P W added to it by the
+//                MMA, the sum into the W tile, which no MMA reads any more, and from there to memory
+//   warps 12-15  one column c of M each, in fp32 registers for the whole item: M's bf16 copy for the
+//                readout (the only rounding of M), M <- γ^n M + U. (U is summed apart from M: the tensor
+//                cores' own accumulation would lose a little of M at every step.)
+//   warps 16-19  (γ w)ᵀ as three bf16 parts into tensor memory (a ring of two 32-token quarters)
+// Except for M's columns all loops stay rolled over blocks of 32 columns: five kinds of warps share the
+// instruction cache, and straight-line code ran at a quarter of an instruction per cycle and warp.
 // Rounded to bf16: P and M's copy, once each, because each meets a bf16 operand and makes a bf16
 // output; γ w enters M as hi + mid + lo, 24 bits together, so that M stays an fp32 state (two parts
 // would put 3e-6 into S_final and dS0, three 1e-7).
@@ -38,11 +41,14 @@ using namespace sm100;
 namespace {
 
 constexpr int kTile = kLaChunk * 128;  // 128 tokens x 128 bytes (64 bf16), 128-byte swizzle: 16 KB
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kRing = 2, kPart = 16;   // γ w ring: 2 quarters x 3 parts x 16 columns
 constexpr uint32_t kColP = 0, kColO = 128, kColU = 256, kColRing = 384;
 
-constexpr int kTable = 32 + kLaChunk;  // per item: γ^(31-j) (reverse: γ^j) of a block's 32 columns; γ^(127-s) (γ^(s+1))
+// An item's powers of γ by distance, with 32 zeros on the side that the mask hides: 0 .. 0 γ^0 .. γ^127, or
+// for a reverse role γ^127 .. γ^0 0 .. 0, so that row i's factor for token s is element la_origin + i - s.
+constexpr int kTable = 32 + kLaChunk;
+__host__ __device__ constexpr int la_origin(bool rev) { return rev ? kLaChunk - 1 : 32; }
 
 enum { kMapX, kMapY, kMapW, kMapOut };
 
@@ -80,14 +86,9 @@ __device__ __forceinline__ uint32_t pair(float a, float b) {
 // Shared memory through its own address space: pointers cut from the aligned base are generic to the
 // compiler, and generic accesses cost a chunk several times its arithmetic (8.0 against 0.6 thousand
 // cycles for P's 128 x 128 factors).
-__device__ __forceinline__ float4 lds4(uint32_t at) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
-  return v;
-}
-__device__ __forceinline__ float2 lds2(uint32_t at) {
-  float2 v;
-  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at));
+__device__ __forceinline__ float lds1(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
   return v;
 }
 __device__ __forceinline__ void sts4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -153,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
   uint64_t* empty = full + NS;                                 // [NS] stage free
   uint64_t* staged = empty + NS;                               // [NS] output tile written
   uint64_t* sc_full = staged + NS;                             // scores in tensor memory
-  uint64_t* p_ready = sc_full + 1;                             // P written, the readout taken
+  uint64_t* p_ready = sc_full + 1;                             // P written, the readout scaled
   uint64_t* m_ready = p_ready + 1;                             // M's copy written
   uint64_t* mx_full = m_ready + 1;                             // the readout in tensor memory, the copy free
   uint64_t* o_full = mx_full + 1;                              // P W in tensor memory, P and the tiles free
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       mbar_init(&staged[i], 4);
     }
     mbar_init(sc_full, 1);
-    mbar_init(p_ready, 4);
+    mbar_init(p_ready, 8);  // warps 4-7: P; warps 8-11: the readout's scaling
     mbar_init(m_ready, 4);
     mbar_init(mx_full, 1);
     mbar_init(o_full, 1);
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     mbar_init(u_free, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&pw_full[i], 1);
-      mbar_init(&pw_empty[i], MODE == 0 ? 8 : 4);  // warps 4-7 (MODE 0) and 12-15
+      mbar_init(&pw_empty[i], MODE == 0 ? 8 : 4);  // warps 4-7 (MODE 0) and 16-19
     }
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
   };
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {
       // ---------------- loads ----------------
       uint32_t it = 0;
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             if (elect_one()) {
 #pragma unroll 1
               for (int ks = 0; ks < kLaChunk / 16; ++ks)
-                mma_bf16_ts(tmem + kColO, tmem + kColP + ks * 8, dMN + sW + ks * 128, id_pw, ks > 0);
+                mma_bf16_ts(tmem + kColO, tmem + kColP + ks * 8, dMN + sW + ks * 128, id_pw, 1u);
               mma_commit(o_full);
             }
             __syncwarp();
@@ -394,81 +395,90 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         const float lg = p.g[t.h] * kLog2e;
         const int rev = t.r->rev;
         float* table = reinterpret_cast<float*>(sm + SM::POW) + (ii & 1) * kTable;
-        table[lane] = la_pow(lg, rev ? lane : 31 - lane);
-        for (int e = lane; e < kLaChunk; e += 32) table[32 + e] = la_pow(lg, rev ? e + 1 : kLaChunk - 1 - e);
+        for (int e = lane; e < kTable; e += 32) {
+          const int d = rev ? kLaChunk - 1 - e : e - 32;
+          table[e] = d >= 0 ? la_pow(lg, d) : 0.f;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&pw_full[ii & 1]);
       }
     }
   } else if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (MODE == 0) {
-      // ---------------- scores -> P, outputs ----------------
+      // ---------------- scores -> P ----------------
       const int wq = warp & 3, row = 32 * wq + lane;
-      const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16);
+      const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16) + kColP;
       uint32_t it = 0, ii = 0;
       bool ok = true;
       for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x, ++ii) {
         const LaItem t = la_item(p, item);
-        const LaRole& r = *t.r;
-        const int rev = r.rev;
-        const uint32_t table = smem_u32(sm) + SM::POW + (ii & 1) * kTable * 4;
-        const float lg = p.g[t.h] * kLog2e;
+        const int rev = t.r->rev;
+        const uint32_t table = smem_u32(sm) + SM::POW + ((ii & 1) * kTable + la_origin(rev) + row) * 4;
+        const float s_intra = t.r->s_inter * t.r->s_u;
         if (!(ok = wait(&pw_full[ii & 1], (ii >> 1) & 1))) break;
-        const float s_intra = r.s_inter * r.s_u;
         for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
-          const int st = it % NS;
-          const uint32_t ph = it & 1;
-          int64_t t0;
-          const int n = la_chunk(t, i, t0);
-          if (!(ok = wait(sc_full, ph))) break;
+          if (!(ok = wait(sc_full, it & 1))) break;
           tc_fence_after();
-          // P's 32 tokens of block blk go to columns 16 blk .., which scores read earlier have left. A block
-          // on one side of the diagonal takes γ^distance as the row's power to the block's nearest column
-          // times the column's from there (both <= 1), the diagonal's own takes it whole.
+          // P's 32 tokens of block blk go to columns 16 blk .., which scores read earlier have left
 #pragma unroll 1
           for (int blk = 0; blk < 4; ++blk) {
             uint32_t w16[16];
             if (rev ? blk >= wq : blk <= wq) {
               float f[32];
-              tmem_ld32(tl + kColP + blk * 32, f);
-              if (blk != wq) {
-                const float rp = la_pow(lg, rev ? blk * 32 - row : row - blk * 32 - 31);
+              tmem_ld32(tl + blk * 32, f);
+              const uint32_t at = table - blk * 128;
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                  const float4 c = lds4(table + j * 4);
-                  f[j] *= rp * c.x;
-                  f[j + 1] *= rp * c.y;
-                  f[j + 2] *= rp * c.z;
-                  f[j + 3] *= rp * c.w;
-                }
-              } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                  const int d = rev ? j - lane : lane - j;
-                  f[j] = d > 0 ? f[j] * ex2_approx(lg * (float)d) : d == 0 ? f[j] : 0.f;
-                }
-              }
+              for (int j = 0; j < 32; ++j) f[j] *= s_intra * lds1(at - j * 4);
 #pragma unroll
               for (int j = 0; j < 16; ++j) w16[j] = pair(f[2 * j], f[2 * j + 1]);
             } else {
 #pragma unroll
               for (int j = 0; j < 16; ++j) w16[j] = 0u;
             }
-            tmem_st16(tl + kColP + blk * 16, w16);
+            tmem_st16(tl + blk * 16, w16);
           }
           tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_ready);
+        }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pw_empty[ii & 1]);
+      }
+      if (!ok) give_up(75);
+    }
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (MODE == 0) {
+      // ---------------- outputs ----------------
+      const int wq = warp & 3, row = 32 * wq + lane;
+      const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16) + kColO;
+      uint32_t it = 0;
+      bool ok = true;
+      for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
+        const LaItem t = la_item(p, item);
+        const LaRole& r = *t.r;
+        const float lg = p.g[t.h] * kLog2e;
+        for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
+          const int st = it % NS;
+          const uint32_t ph = it & 1;
+          int64_t t0;
+          const int n = la_chunk(t, i, t0);
+          const float f_in = r.s_inter * la_pow(lg, r.rev ? max(n - 1 - row, 0) : row + 1);
           if (!(ok = wait(mx_full, ph))) break;
           tc_fence_after();
-          float o[DW];
-          const float f_in = r.s_inter * la_pow(lg, rev ? max(n - 1 - row, 0) : row + 1);
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < DW / 32; ++k) {
             float f[32];
-            tmem_ld32(tl + kColO + k * 32, f);
+            uint32_t u[32];
+            tmem_ld32(tl + k * 32, f);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[k * 32 + j] = f_in * f[j];
+            for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(f_in * f[j]);
+            tmem_st32(tl + k * 32, u);
           }
+          tmem_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(p_ready);
@@ -477,12 +487,10 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           const uint32_t tile = smem_u32(sm) + st * SM::STAGE + SM::W;
           const bool whole = !r.out_f32 && (n == kLaChunk || t0 + n == p.L);
           const int64_t at = t.b * r.out_sb + (t0 + row) * r.out_st + (int64_t)t.h * r.dw;
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < DW / 32; ++k) {
             float f[32];
-            tmem_ld32(tl + kColO + k * 32, f);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] = fmaf(s_intra, f[j], o[k * 32 + j]);
+            tmem_ld32(tl + k * 32, f);
             if (whole) {
 #pragma unroll
               for (int c = 0; c < 4; ++c)
@@ -514,14 +522,11 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             mbar_arrive(&staged[st]);
           }
         }
-        if (!ok) break;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pw_empty[ii & 1]);
       }
-      if (!ok) give_up(75);
+      if (!ok) give_up(78);
     }
-  } else if (warp < 12) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+  } else if (warp < 16) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     // ---------------- the state ----------------
     const int wq = warp & 3, col = 32 * wq + lane;  // column of M = lane of U
     const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16);
@@ -548,8 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         int64_t t0;
         const int n = la_chunk(t, i, t0);
         if (MODE == 0) {
-          // M's copy; the readout of the chunk before has taken the last one
-          if (it > 0 && !(ok = wait(mx_full, (it & 1) ^ 1))) break;
+          // M's copy; the readout of the chunk before has taken the last one (its MMAs come before U's)
           if (active) {
 #pragma unroll
             for (int c = 0; c < DX / 8; ++c)
@@ -569,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             float f[32];
             tmem_ld32(tl + kColU + k * 32, f);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) m[k * 32 + j] = fmaf(g, m[k * 32 + j], r.s_u * f[j]);
+            for (int j = 0; j < 32; ++j) m[k * 32 + j] = fmaf(g, m[k * 32 + j], f[j]);
           }
         }
         tc_fence_before();
@@ -603,8 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x, ++ii) {
       const LaItem t = la_item(p, item);
       const int rev = t.r->rev;
-      const uint32_t table = smem_u32(sm) + SM::POW + (ii & 1) * kTable * 4 + 128;
-      const float lg = p.g[t.h] * kLog2e;
+      const uint32_t table = smem_u32(sm) + SM::POW + ((ii & 1) * kTable + la_origin(rev)) * 4;
+      const float f_w = rev ? t.r->s_u * la_pow(p.g[t.h] * kLog2e, 1) : t.r->s_u;
       if (!(ok = wait(&pw_full[ii & 1], (ii >> 1) & 1))) break;
       for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
         const int st = it % NS;
@@ -624,11 +628,12 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             uint32_t keep[4];
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-              const int s = 32 * qr + 8 * g + 2 * (lane & 3);
-              wt[g] = lds2(table + s * 4);
+              // γ^(n-1-s), reverse γ γ^s; tokens behind the last chunk's end count as zeros whatever they hold
+              const int s = 32 * qr + 8 * g + 2 * (lane & 3), e = rev ? s : max(n - 2 - s, -1);
+              const float a0 = lds1(table + (rev ? -e : e + 1) * 4), a1 = lds1(table + (rev ? -e - 1 : e) * 4);
+              wt[g] = make_float2(a0 * f_w, a1 * f_w);
               keep[g] = 0xffffffffu;
-              if (n < kLaChunk) {  // the last chunk's decays count from its last token; behind it nothing is read
-                if (!rev) wt[g] = make_float2(la_pow(lg, max(n - 1 - s, 0)), la_pow(lg, max(n - 2 - s, 0)));
+              if (n < kLaChunk) {
                 keep[g] = (s < n ? 0xffffu : 0u) | (s + 1 < n ? 0xffff0000u : 0u);
               }
             }
