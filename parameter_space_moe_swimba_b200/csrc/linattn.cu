@@ -164,13 +164,20 @@ __global__ void __launch_bounds__(256) la_chain_kernel(const __grid_constant__ L
   float* seg = r.seg + bh * p.nseg * size + e;
   const int64_t own = bh * size + (int64_t)j * r.sj + (int64_t)c * r.sc;
   float m = r.M0 ? r.M0[own] : 0.f;
-  for (int s = 0; s < p.nseg; ++s) {
-    int c0, c1;
-    la_segment(p, len, s, r.rev, c0, c1);
-    const int64_t n = max((int64_t)0, min((int64_t)c1 * kLaChunk, len) - (int64_t)c0 * kLaChunk);
-    const float end = seg[(int64_t)s * size];
-    seg[(int64_t)s * size] = m;
-    if (n > 0) m = fmaf(la_pow(lg, (int)n), m, end);
+  constexpr int kBatch = 8;  // loads in flight: the stores in between keep the compiler from moving them up
+  for (int s0 = 0; s0 < p.nseg; s0 += kBatch) {
+    float end[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) end[i] = s0 + i < p.nseg ? seg[(int64_t)(s0 + i) * size] : 0.f;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (s0 + i >= p.nseg) break;
+      int c0, c1;
+      la_segment(p, len, s0 + i, r.rev, c0, c1);
+      const int64_t n = max((int64_t)0, min((int64_t)c1 * kLaChunk, len) - (int64_t)c0 * kLaChunk);
+      seg[(int64_t)(s0 + i) * size] = m;
+      if (n > 0) m = fmaf(la_pow(lg, (int)n), m, end[i]);
+    }
   }
   if (r.M_end) r.M_end[own] = m;
 }

@@ -18,13 +18,13 @@
 //   warps 12-15  one column c of M each, in fp32 registers for the whole item: M's bf16 copy for the
 //                readout (the only rounding of M), M <- γ^n M + U. (U is summed apart from M: the tensor
 //                cores' own accumulation would lose a little of M at every step.)
-//   warps 16-19  (γ w)ᵀ as three bf16 parts into tensor memory (a ring of two 32-token quarters)
+//   warps 16-19  (γ w)ᵀ as three bf16 parts into tensor memory (a ring of 16-token steps)
 // Except for M's columns all loops stay rolled over blocks of 32 columns: five kinds of warps share the
 // instruction cache, and straight-line code ran at a quarter of an instruction per cycle and warp.
 // Rounded to bf16: P and M's copy, once each, because each meets a bf16 operand and makes a bf16
 // output; γ w enters M as hi + mid + lo, 24 bits together, so that M stays an fp32 state (two parts
 // would put 3e-6 into S_final and dS0, three 1e-7).
-// Tensor memory: scores / P 128 columns, out 128, U dx, the γ w ring 96.
+// Tensor memory: scores / P 128 columns, out 128, U dx, the γ w ring 120.
 // Every wait is bounded; a wait that runs out records SWIMBA_ERR_TIMEOUT, and the CTA drains and exits.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -42,7 +42,9 @@ namespace {
 
 constexpr int kTile = kLaChunk * 128;  // 128 tokens x 128 bytes (64 bf16), 128-byte swizzle: 16 KB
 constexpr int kThreads = 640;
-constexpr int kRing = 2, kPart = 16;   // γ w ring: 2 quarters x 3 parts x 16 columns
+// γ w ring: 5 slots of 16 tokens (one MMA step) x 3 parts x 8 columns. Slots of 16 tokens rather than 32
+// let the warps that fill it refill a slot in half the time that its MMAs and theirs keep it busy.
+constexpr int kRing = 5, kPart = 8, kStep = 16, kSteps = kLaChunk / kStep;
 constexpr uint32_t kColP = 0, kColO = 128, kColU = 256, kColRing = 384;
 
 // An item's powers of γ by distance, with 32 zeros on the side that the mask hides: 0 .. 0 γ^0 .. γ^127, or
@@ -101,10 +103,10 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t at, uint32_t (&r)[4])
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(at));
 }
-// 16 lanes x 16 columns: thread t's r[2 k] is lane t / 4, r[2 k + 1] lane t / 4 + 8, column 4 k + t % 4.
-__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+// 16 lanes x 8 columns: thread t's r[2 k] is lane t / 4, r[2 k + 1] lane t / 4 + 8, column 4 k + t % 4.
+__device__ __forceinline__ void tmem_st_16x128b_x2(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
                : "memory");
 }
 
@@ -259,11 +261,10 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       constexpr uint32_t id_sc = idesc_bf16(128, 128, false), id_mx = idesc_bf16(128, DW, false),
                          id_u = idesc_bf16(128, DX, true), id_pw = idesc_bf16(128, DW, true);
       const uint32_t base = smem_u32(sm);
-      // descriptors of address 0, to which a tile's address / 16 is added; the loops stay rolled, so that
-      // the issuing warp's few instructions stay in the instruction cache beside the other warps'
+      // descriptors of address 0, to which a tile's address / 16 is added
       const uint64_t dK = smem_desc(0, 16, 1024, kLayoutSW128), dMN = smem_desc(0, kTile, 1024, kLayoutSW128);
       auto kstep = [](int ks, int box) { return (uint32_t)((ks >> 2) * (box >> 4) + (ks & 3) * 2); };
-      uint32_t it = 0;
+      uint32_t it = 0, slot = 0, ring_phase = 0;
       bool ok = true;
       for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
         const LaItem t = la_item(p, item);
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             if (it > 0 && !(ok = wait(o_full, ph ^ 1))) break;
             tc_fence_after();
             if (elect_one()) {
-#pragma unroll 1
+#pragma unroll
               for (int ks = 0; ks < DX / 16; ++ks)
                 mma_bf16(tmem + kColP, dK + sX + kstep(ks, kTile), dK + sY + kstep(ks, kTile), id_sc, ks > 0);
               mma_commit(sc_full);
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             if (it > 0 && !(ok = wait(o_free, ph ^ 1))) break;
             tc_fence_after();
             if (elect_one()) {
-#pragma unroll 1
+#pragma unroll
               for (int ks = 0; ks < DX / 16; ++ks)
                 mma_bf16(tmem + kColO, dK + sX + kstep(ks, kTile), dK + ((base + SM::M) >> 4) + kstep(ks, DW * 128), id_mx,
                          ks > 0);
@@ -310,21 +311,24 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             }
             __syncwarp();
           }
-          // U = Σ_s (γ w_s) y_sᵀ, 32 tokens at a time
+          // U = Σ_s (γ w_s) y_sᵀ, 16 tokens at a time
           if (it > 0 && !(ok = wait(u_free, ph ^ 1))) break;
 #pragma unroll 1
-          for (int qr = 0; qr < 4; ++qr) {
-            const uint32_t slot = qr & 1, use = it * 2 + (qr >> 1);
-            if (!(ok = wait(&ring_full[slot], use & 1))) break;
+          for (int k = 0; k < kSteps; ++k) {
+            if (!(ok = wait(&ring_full[slot], ring_phase))) break;
             tc_fence_after();
             if (elect_one()) {
-#pragma unroll 1
-              for (int k = 0; k < 6; ++k)  // part k / 2, tokens 16 (k % 2) ..
-                mma_bf16_ts(tmem + kColU, tmem + kColRing + slot * 3 * kPart + k * 8, dMN + sY + (qr * 2 + (k & 1)) * 128, id_u,
-                            (qr | k) != 0);
+#pragma unroll
+              for (int part = 0; part < 3; ++part)
+                mma_bf16_ts(tmem + kColU, tmem + kColRing + slot * 3 * kPart + part * kPart, dMN + sY + k * (kStep * 8), id_u,
+                            (k | part) != 0);
               mma_commit(&ring_empty[slot]);
             }
             __syncwarp();
+            if (++slot == kRing) {
+              slot = 0;
+              ring_phase ^= 1;
+            }
           }
           if (!ok) break;
           if (elect_one()) {
@@ -336,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             if (!(ok = wait(p_ready, ph))) break;
             tc_fence_after();
             if (elect_one()) {
-#pragma unroll 1
+#pragma unroll
               for (int ks = 0; ks < kLaChunk / 16; ++ks)
                 mma_bf16_ts(tmem + kColO, tmem + kColP + ks * 8, dMN + sW + ks * 128, id_pw, 1u);
               mma_commit(o_full);
@@ -549,36 +553,48 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         for (int j = 0; j < DX; ++j)
           m[j] = (start != nullptr && j < r.dx && col < r.dw) ? start[(int64_t)j * sj + (int64_t)col * sc] : 0.f;
       }
-      for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
+      // M's bf16 copy of 32 columns (the readout of the chunk before has taken the last one: its MMAs come
+      // before U's)
+      auto copy32 = [&](int k) {
+#pragma unroll
+        for (int c = 4 * k; c < 4 * k + 4; ++c)
+          sts4(smem_u32(sm) + SM::M + (c >> 3) * (DW * 128) + swz16(col, c & 7), pair(m[8 * c], m[8 * c + 1]),
+               pair(m[8 * c + 2], m[8 * c + 3]), pair(m[8 * c + 4], m[8 * c + 5]), pair(m[8 * c + 6], m[8 * c + 7]));
+      };
+      auto copied = [&]() {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(m_ready);
+      };
+      const int chunks = t.c1 - t.c0;
+      if (MODE == 0 && chunks > 0) {
+        if (active) {
+#pragma unroll
+          for (int k = 0; k < DX / 32; ++k) copy32(k);
+        }
+        copied();
+      }
+      for (int i = 0; i < chunks; ++i, ++it) {
         int64_t t0;
         const int n = la_chunk(t, i, t0);
-        if (MODE == 0) {
-          // M's copy; the readout of the chunk before has taken the last one (its MMAs come before U's)
-          if (active) {
-#pragma unroll
-            for (int c = 0; c < DX / 8; ++c)
-              sts4(smem_u32(sm) + SM::M + (c >> 3) * (DW * 128) + swz16(col, c & 7), pair(m[8 * c], m[8 * c + 1]),
-                   pair(m[8 * c + 2], m[8 * c + 3]), pair(m[8 * c + 4], m[8 * c + 5]), pair(m[8 * c + 6], m[8 * c + 7]));
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(m_ready);
-        }
+        const float g = n == kLaChunk ? g_all : la_pow(lg, n);
+        const bool more = MODE == 0 && i + 1 < chunks;
         if (!(ok = wait(u_full, it & 1))) break;
         tc_fence_after();
         if (active) {
-          const float g = n == kLaChunk ? g_all : la_pow(lg, n);
 #pragma unroll
           for (int k = 0; k < DX / 32; ++k) {
             float f[32];
             tmem_ld32(tl + kColU + k * 32, f);
 #pragma unroll
             for (int j = 0; j < 32; ++j) m[k * 32 + j] = fmaf(g, m[k * 32 + j], f[j]);
+            if (more) copy32(k);
           }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(u_free);
+        if (more) copied();
       }
       if (!ok) break;
       if (col < r.dw && (MODE == 1 || (p.nseg == 1 && r.M_end != nullptr))) {
@@ -597,12 +613,12 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16);
     const bool active = 32 * wq < DW;
     if (!active) {  // those rows stay zero
-      const uint32_t z[16] = {};
-#pragma unroll
-      for (int k = 0; k < kRing * 3; ++k) tmem_st16(tl + kColRing + k * kPart, z);
+      const uint32_t z[8] = {};
+#pragma unroll 1
+      for (int k = 0; k < kRing * 3; ++k) tmem_st8(tl + kColRing + k * kPart, z);
       tmem_wait_st();
     }
-    uint32_t it = 0, ii = 0;
+    uint32_t it = 0, ii = 0, slot = 0, ring_phase = 0;
     bool ok = true;
     for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x, ++ii) {
       const LaItem t = la_item(p, item);
@@ -615,58 +631,56 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         int64_t t0;
         const int n = la_chunk(t, i, t0);
         if (!(ok = wait(&full[st], (it / NS) & 1))) break;
-        // 32 tokens at a time: 8 x 8 blocks of W, transposed on the way to the registers, where thread t
+        // 16 tokens at a time: 8 x 8 blocks of W, transposed on the way to the registers, where thread t
         // holds channel t / 4 of tokens 2 (t % 4) + 0..1, scaled, split and stored in that form
-        const uint32_t tw = smem_u32(sm) + st * SM::STAGE + SM::W + (wq >> 1) * kTile + (lane & 7) * 128;
+        const uint32_t tw = smem_u32(sm) + st * SM::STAGE + SM::W + (wq >> 1) * kTile + ((lane & 7) + 8 * (lane >> 4)) * 128;
 #pragma unroll 1
-        for (int qr = 0; qr < 4; ++qr) {
-          const uint32_t slot = qr & 1, use = it * 2 + (qr >> 1);
-          if (!(ok = wait(&ring_empty[slot], (use & 1) ^ 1))) break;
+        for (int k = 0; k < kSteps; ++k) {
+          if (!(ok = wait(&ring_empty[slot], ring_phase ^ 1))) break;
           tc_fence_after();
           if (active) {
-            float2 wt[4];
-            uint32_t keep[4];
+            uint32_t raw[2][4];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
+            for (int half = 0; half < 2; ++half)  // 16 channels: matrices (tokens, channels) (0, 0), (0, 8), (8, 0), (8, 8)
+              ldmatrix_x4_trans(tw + k * (kStep * 128) + ((((wq & 1) * 4 + half * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4),
+                                raw[half]);
+            float2 wt[2];
+            uint32_t keep[2];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
               // γ^(n-1-s), reverse γ γ^s; tokens behind the last chunk's end count as zeros whatever they hold
-              const int s = 32 * qr + 8 * g + 2 * (lane & 3), e = rev ? s : max(n - 2 - s, -1);
+              const int s = kStep * k + 8 * g + 2 * (lane & 3), e = rev ? s : max(n - 2 - s, -1);
               const float a0 = lds1(table + (rev ? -e : e + 1) * 4), a1 = lds1(table + (rev ? -e - 1 : e) * 4);
               wt[g] = make_float2(a0 * f_w, a1 * f_w);
-              keep[g] = 0xffffffffu;
-              if (n < kLaChunk) {
-                keep[g] = (s < n ? 0xffffu : 0u) | (s + 1 < n ? 0xffff0000u : 0u);
-              }
+              keep[g] = (s < n ? 0xffffu : 0u) | (s + 1 < n ? 0xffff0000u : 0u);
             }
-#pragma unroll 1
+#pragma unroll
             for (int half = 0; half < 2; ++half) {
-              uint32_t hi[8], mid[8], lo[8];
+              uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
-              for (int g2 = 0; g2 < 2; ++g2) {  // matrices (8 tokens, 8 channels): (0, 0), (0, 1), (1, 0), (1, 1)
-                uint32_t raw[4];
-                const int chunk = ((wq & 1) * 4 + half * 2 + ((lane >> 3) & 1)) ^ (lane & 7);
-                ldmatrix_x4_trans(tw + (32 * qr + 16 * g2 + 8 * (lane >> 4)) * 128 + (chunk << 4), raw);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  // three truncated parts of 8 bits each: their sum is the product's 24 bits
-                  const int g = 2 * g2 + (k >> 1), d = 4 * g2 + k;
-                  const uint32_t v = raw[k] & keep[g];
-                  const float v0 = bf16lo(v) * wt[g].x, v1 = bf16hi(v) * wt[g].y;
-                  hi[d] = high_halves(v0, v1);
-                  const float r0 = v0 - top_bits(v0), r1 = v1 - top_bits(v1);
-                  mid[d] = high_halves(r0, r1);
-                  lo[d] = high_halves(r0 - top_bits(r0), r1 - top_bits(r1));
-                }
+              for (int d = 0; d < 4; ++d) {
+                // three truncated parts of 8 bits each: their sum is the product's 24 bits
+                const uint32_t v = raw[half][d] & keep[d >> 1];
+                const float v0 = bf16lo(v) * wt[d >> 1].x, v1 = bf16hi(v) * wt[d >> 1].y;
+                hi[d] = high_halves(v0, v1);
+                const float r0 = v0 - top_bits(v0), r1 = v1 - top_bits(v1);
+                mid[d] = high_halves(r0, r1);
+                lo[d] = high_halves(r0 - top_bits(r0), r1 - top_bits(r1));
               }
               const uint32_t at = tl + ((uint32_t)(16 * half) << 16) + kColRing + slot * 3 * kPart;
-              tmem_st_16x128b_x4(at, hi);
-              tmem_st_16x128b_x4(at + kPart, mid);
-              tmem_st_16x128b_x4(at + 2 * kPart, lo);
+              tmem_st_16x128b_x2(at, hi);
+              tmem_st_16x128b_x2(at + kPart, mid);
+              tmem_st_16x128b_x2(at + 2 * kPart, lo);
             }
             tmem_wait_st();
           }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&ring_full[slot]);
+          if (++slot == kRing) {
+            slot = 0;
+            ring_phase ^= 1;
+          }
         }
         if (!ok) break;
       }
