@@ -8,17 +8,20 @@
 // A reverse role mirrors the exponents: γ^(s-i) for s >= i, γ^(n-1-i), γ^(s+1).
 //
 // Persistent, one CTA per SM; an item is one (role, segment, sequence, head), its chunks in order:
-//   warp 0       TMA loads of the X, Y, W tiles into a ring of stages
-//   warp 1       issues every MMA
-//   warp 2       TMA stores of the finished output tiles
-//   warp 3       the head's table of powers γ^0 .. γ^128
+//   warp 0       TMA loads of the X, Y, W tiles into a ring each; the item's table of powers of γ
+//   warp 1       the MMAs of scores, readout and outputs
+//   warp 2       the MMAs of U. (A wait costs an issuing warp about 170 cycles and a commit 70, as much as
+//                two and one of these MMAs, and few MMAs queue up: one warp for both made every wait
+//                a gap in the tensor cores' work.)
+//   warp 3       TMA stores of the finished output tiles
 //   warps 4-7    scores -> P: bf16, in place, the A operand of P W; one row i = TMEM lane each
 //   warps 8-11   the outputs' rows: the carried state's readout scaled in place, P W added to it by the
 //                MMA, the sum into the W tile, which no MMA reads any more, and from there to memory
 //   warps 12-15  one column c of M each, in fp32 registers for the whole item: M's bf16 copy for the
 //                readout (the only rounding of M), M <- γ^n M + U. (U is summed apart from M: the tensor
 //                cores' own accumulation would lose a little of M at every step.)
-//   warps 16-19  (γ w)ᵀ as three bf16 parts into tensor memory (a ring of 16-token steps)
+//   warps 16-23  (γ w)ᵀ as three bf16 parts into tensor memory (a ring of 16-token steps, dealt in turn to
+//                two sets of four warps)
 // Except for M's columns all loops stay rolled over blocks of 32 columns: five kinds of warps share the
 // instruction cache, and straight-line code ran at a quarter of an instruction per cycle and warp.
 // Rounded to bf16: P and M's copy, once each, because each meets a bf16 operand and makes a bf16
@@ -41,7 +44,7 @@ using namespace sm100;
 namespace {
 
 constexpr int kTile = kLaChunk * 128;  // 128 tokens x 128 bytes (64 bf16), 128-byte swizzle: 16 KB
-constexpr int kThreads = 640;
+constexpr int kThreads = 768;
 // γ w ring: 5 slots of 16 tokens (one MMA step) x 3 parts x 8 columns. Slots of 16 tokens rather than 32
 // let the warps that fill it refill a slot in half the time that its MMAs and theirs keep it busy.
 constexpr int kRing = 5, kPart = 8, kStep = 16, kSteps = kLaChunk / kStep;
@@ -57,24 +60,23 @@ enum { kMapX, kMapY, kMapW, kMapOut };
 struct LaTcArgs {
   CUtensorMap map[kLaMaxRoles][4];
   LaParams p;
-  int64_t items;
+  uint32_t items;
 };
 
 template <int DX, int DW, int MODE>
 struct LaSmem {
   static constexpr int XB = DX / 64, WB = DW / 64;
-  static constexpr int X = 0, Y = MODE == 0 ? XB * kTile : 0, W = Y + XB * kTile;  // inside a stage
-  static constexpr int STAGE = W + WB * kTile;
+  static constexpr int TX = MODE == 0 ? XB * kTile : 0, TY = XB * kTile, TW = WB * kTile;  // one tile of each
   static constexpr int COPY = MODE == 0 ? DX * DW * 2 : 0;  // M's bf16 copy, [dw rows][dx], K-major
-  static constexpr int ROOM = 229376 - COPY;
-  static constexpr int NS = ROOM / STAGE < 4 ? ROOM / STAGE : 4;
-  static constexpr int M = NS * STAGE;
+  // Tiles in flight. An X tile is free after two MMAs, a Y tile after U, a W tile only when the outputs
+  // that replace it have left; so W gets the most.
+  static constexpr int NX = DX == 128 && DW == 128 ? 1 : 2, NY = DX == 64 ? 3 : 2, NW = DW == 128 ? 3 : 4;
+  static constexpr int X = 0, Y = NX * TX, W = Y + NY * TY, M = W + NW * TW;
   static constexpr int POW = M + COPY;              // 2 x kTable floats
   static constexpr int BAR = POW + 2 * kTable * 4;  // barriers
-  static constexpr int NBAR = 3 * NS + 6 + 2 * kRing + 2 + 4 + 1;
+  static constexpr int NBAR = 2 * NX + 2 * NY + 4 * NW + 6 + 2 * kRing + 2 + 4 + 2 + 2;
   static constexpr int MISC = BAR + NBAR * 8;
   static constexpr int BYTES = MISC + 16;
-  static_assert(NS >= 2, "two stages");
   static_assert(BYTES + 1024 <= 232448, "shared memory of one CTA");
 };
 
@@ -122,15 +124,15 @@ struct LaItem {
   int64_t bh, len;
 };
 
-__device__ __forceinline__ LaItem la_item(const LaParams& p, int64_t item) {
+__device__ __forceinline__ LaItem la_item(const LaParams& p, uint32_t item) {
   LaItem t;
-  t.role = (int)(item % p.n_roles);
-  item /= p.n_roles;
-  t.seg = (int)(item % p.nseg);
-  t.bh = item / p.nseg;
+  const uint32_t rest = item / (uint32_t)p.n_roles, bh = rest / (uint32_t)p.nseg;
+  t.role = (int)(item - rest * p.n_roles);
+  t.seg = (int)(rest - bh * p.nseg);
+  t.bh = bh;
   t.r = &p.role[t.role];
-  t.b = (int)(t.bh / p.H);
-  t.h = (int)(t.bh % p.H);
+  t.b = (int)(bh / (uint32_t)p.H);
+  t.h = (int)bh - t.b * p.H;
   t.len = la_len(p, t.b);
   la_segment(p, t.len, t.seg, t.r->rev, t.c0, t.c1);
   return t;
@@ -149,16 +151,21 @@ __device__ __forceinline__ int la_chunk(const LaItem& t, int i, int64_t& t0) {
 template <int DX, int DW, int MODE>
 __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constant__ LaTcArgs a) {
   using SM = LaSmem<DX, DW, MODE>;
-  constexpr int NS = SM::NS;
+  constexpr int NX = SM::NX, NY = SM::NY, NW = SM::NW;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + SM::BAR);  // [NS] tiles landed
-  uint64_t* empty = full + NS;                                 // [NS] stage free
-  uint64_t* staged = empty + NS;                               // [NS] output tile written
-  uint64_t* sc_full = staged + NS;                             // scores in tensor memory
+  uint64_t* x_full = reinterpret_cast<uint64_t*>(sm + SM::BAR);  // [NX] tile landed
+  uint64_t* x_empty = x_full + NX;                               // [NX] tile free
+  uint64_t* y_full = x_empty + NX;                               // [NY]
+  uint64_t* y_empty = y_full + NY;                               // [NY]
+  uint64_t* w_full = y_empty + NY;                               // [NW]
+  uint64_t* w_empty = w_full + NW;                               // [NW]
+  uint64_t* staged = w_empty + NW;                               // [NW] outputs in the W tile
+  uint64_t* w_read = staged + NW;                                // [NW] (γ w)ᵀ of the tile has been used
+  uint64_t* sc_full = w_read + NW;                             // scores in tensor memory
   uint64_t* p_ready = sc_full + 1;                             // P written, the readout scaled
   uint64_t* m_ready = p_ready + 1;                             // M's copy written
-  uint64_t* mx_full = m_ready + 1;                             // the readout in tensor memory, the copy free
+  uint64_t* mx_full = m_ready + 1;                             // the readout in tensor memory; X and the copy free
   uint64_t* o_full = mx_full + 1;                              // P W in tensor memory, P and the tiles free
   uint64_t* o_free = o_full + 1;                               // out columns read
   uint64_t* ring_full = o_free + 1;                            // [kRing]
@@ -167,18 +174,18 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
   uint64_t* u_free = u_full + 1;                               // U read
   uint64_t* pw_full = u_free + 1;                              // [2]
   uint64_t* pw_empty = pw_full + 2;                            // [2]
-  uint64_t* done = pw_empty + 2;
+  // [2] zeros behind a sequence's end written, in turn: warp 1 can be two such chunks ahead of warp 2's wait
+  uint64_t* fixed = pw_empty + 2;
+  uint64_t* done = fixed + 2;                                  // [2]
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + SM::MISC);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + SM::MISC + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const LaParams& p = a.p;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
-      mbar_init(&staged[i], 4);
-    }
+    for (int i = 0; i < NX; ++i) mbar_init(&x_full[i], 1), mbar_init(&x_empty[i], 1);
+    for (int i = 0; i < NY; ++i) mbar_init(&y_full[i], 1), mbar_init(&y_empty[i], MODE == 0 ? 2 : 1);
+    for (int i = 0; i < NW; ++i) mbar_init(&w_full[i], 1), mbar_init(&w_empty[i], 1), mbar_init(&staged[i], 4), mbar_init(&w_read[i], 1);
     mbar_init(sc_full, 1);
     mbar_init(p_ready, 8);  // warps 4-7: P; warps 8-11: the readout's scaling
     mbar_init(m_ready, 4);
@@ -193,9 +200,12 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     mbar_init(u_free, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&pw_full[i], 1);
-      mbar_init(&pw_empty[i], MODE == 0 ? 8 : 4);  // warps 4-7 (MODE 0) and 16-19
+      mbar_init(&pw_empty[i], MODE == 0 ? 12 : 8);  // warps 4-7 (MODE 0) and 16-23
     }
-    mbar_init(done, 1);
+    mbar_init(&fixed[0], 1);
+    mbar_init(&fixed[1], 1);
+    mbar_init(&done[0], 1);
+    mbar_init(&done[1], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -219,44 +229,57 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {
       // ---------------- loads ----------------
-      uint32_t it = 0;
+      uint32_t it = 0, ii = 0;
       bool ok = true;
-      for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
+      for (uint32_t item = blockIdx.x; item < a.items && ok; item += gridDim.x, ++ii) {
         const LaItem t = la_item(p, item);
         const CUtensorMap* map = a.map[t.role];
+        if (!(ok = wait(&pw_empty[ii & 1], ((ii >> 1) & 1) ^ 1))) break;
+        {
+          const float lg = p.g[t.h] * kLog2e;
+          float* table = reinterpret_cast<float*>(sm + SM::POW) + (ii & 1) * kTable;
+          for (int e = lane; e < kTable; e += 32) {
+            const int d = t.r->rev ? kLaChunk - 1 - e : e - 32;
+            table[e] = d >= 0 ? la_pow(lg, d) : 0.f;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&pw_full[ii & 1]);
+        }
         for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
-          const int st = it % NS;
           int64_t t0;
           la_chunk(t, i, t0);
-          if (!wait(&empty[st], ((it / NS) & 1) ^ 1)) {
-            ok = false;
-            break;
+          auto load = [&](int boxes, int at, const CUtensorMap* m, uint64_t* bar, int div) {
+            mbar_arrive_expect_tx(bar, boxes * kTile);
+            for (int k = 0; k < boxes; ++k) tma_load_4d(sm + at + k * kTile, m, bar, 64 * k, t.h / div, (int)t0, t.b);
+          };
+          // in the order in which the tiles come free
+          if (MODE == 0) {
+            if (!(ok = wait(&x_empty[it % NX], ((it / NX) & 1) ^ 1))) break;
+            if (elect_one()) load(SM::XB, SM::X + (it % NX) * SM::TX, &map[kMapX], &x_full[it % NX], t.r->x.div);
           }
-          if (elect_one()) {
-            uint8_t* s = sm + st * SM::STAGE;
-            mbar_arrive_expect_tx(&full[st], SM::STAGE);
-#pragma unroll
-            for (int k = 0; k < SM::XB; ++k) {
-              if (MODE == 0) tma_load_4d(s + SM::X + k * kTile, &map[kMapX], &full[st], 64 * k, t.h / t.r->x.div, (int)t0, t.b);
-              tma_load_4d(s + SM::Y + k * kTile, &map[kMapY], &full[st], 64 * k, t.h / t.r->y.div, (int)t0, t.b);
-            }
-#pragma unroll
-            for (int k = 0; k < SM::WB; ++k)
-              tma_load_4d(s + SM::W + k * kTile, &map[kMapW], &full[st], 64 * k, t.h / t.r->w.div, (int)t0, t.b);
-          }
+          if (!(ok = wait(&y_empty[it % NY], ((it / NY) & 1) ^ 1))) break;
+          if (elect_one()) load(SM::XB, SM::Y + (it % NY) * SM::TY, &map[kMapY], &y_full[it % NY], t.r->y.div);
+          if (!(ok = wait(&w_empty[it % NW], ((it / NW) & 1) ^ 1))) break;
+          if (elect_one()) load(SM::WB, SM::W + (it % NW) * SM::TW, &map[kMapW], &w_full[it % NW], t.r->w.div);
           __syncwarp();
         }
       }
       if (!ok) give_up(71);
-      // copies that may still be landing (after an orderly end every one has been waited for)
+      // copies that may still be landing (after an orderly end every one has been waited for); `it` counts
+      // the chunks whose copies were all issued, the next one's may be
       if (*abort_flag) {
-        for (uint32_t k = it > (uint32_t)NS ? it - NS : 0; k < it; ++k) {
-          const uint64_t w0 = globaltimer_ns();
-          while (!mbar_try_wait(&full[k % NS], (k / NS) & 1) && globaltimer_ns() - w0 < kWaitLimitNs) {
+        auto drain = [&](uint64_t* bar, uint32_t n) {
+          for (uint32_t k = it + 1 > n ? it + 1 - n : 0; k <= it; ++k) {
+            const uint64_t w0 = globaltimer_ns();
+            while (!mbar_try_wait(&bar[k % n], (k / n) & 1) && globaltimer_ns() - w0 < kWaitLimitNs / 16) {
+            }
           }
-        }
+        };
+        if (MODE == 0) drain(x_full, NX);
+        drain(y_full, NY);
+        drain(w_full, NW);
       }
-    } else if (warp == 1) {
+    } else if (warp == 2 || (MODE == 0 && warp == 1)) {
       // ---------------- MMAs ----------------
       constexpr uint32_t id_sc = idesc_bf16(128, 128, false), id_mx = idesc_bf16(128, DW, false),
                          id_u = idesc_bf16(128, DX, true), id_pw = idesc_bf16(128, DW, true);
@@ -264,32 +287,63 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       // descriptors of address 0, to which a tile's address / 16 is added
       const uint64_t dK = smem_desc(0, 16, 1024, kLayoutSW128), dMN = smem_desc(0, kTile, 1024, kLayoutSW128);
       auto kstep = [](int ks, int box) { return (uint32_t)((ks >> 2) * (box >> 4) + (ks & 3) * 2); };
-      uint32_t it = 0, slot = 0, ring_phase = 0;
+      uint32_t it = 0, slot = 0, ring_phase = 0, fixes = 0;
       bool ok = true;
-      for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
+      for (uint32_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
         const LaItem t = la_item(p, item);
         for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
-          const int st = it % NS;
           const uint32_t ph = it & 1;
           int64_t t0;
           const int n = la_chunk(t, i, t0);
-          const uint32_t sX = (base + st * SM::STAGE + SM::X) >> 4, sY = (base + st * SM::STAGE + SM::Y) >> 4,
-                         sW = (base + st * SM::STAGE + SM::W) >> 4;
-          if (!(ok = wait(&full[st], (it / NS) & 1))) break;
-          if (n < kLaChunk && t0 + n < p.L) {
-            // tokens behind the sequence's end that lie in memory: whatever they hold, they are zeros here
-            // (behind the tensor's end the copies have filled in zeros)
-            uint8_t* s = sm + st * SM::STAGE + SM::Y;
+          const uint32_t sX = (base + SM::X + (it % NX) * SM::TX) >> 4, sY = (base + SM::Y + (it % NY) * SM::TY) >> 4,
+                         sW = (base + SM::W + (it % NW) * SM::TW) >> 4;
+          // tokens behind the sequence's end that lie in memory: whatever they hold, they are zeros here
+          // (behind the tensor's end the copies have filled in zeros)
+          const bool fix = n < kLaChunk && t0 + n < p.L;
+          if (!(ok = wait(&y_full[it % NY], (it / NY) & 1))) break;
+          if (fix && (MODE == 1 || warp == 1)) {
+            if (!(ok = wait(&w_full[it % NW], (it / NW) & 1))) break;
             for (int k = lane; k < (kLaChunk - n) * 8 * (SM::XB + SM::WB); k += 32) {
               const int tile = k / ((kLaChunk - n) * 8), at = k - tile * (kLaChunk - n) * 8;
-              *reinterpret_cast<uint4*>(s + tile * kTile + n * 128 + at * 16) = make_uint4(0, 0, 0, 0);
+              uint8_t* s = tile < SM::XB ? sm + SM::Y + (it % NY) * SM::TY + tile * kTile
+                                         : sm + SM::W + (it % NW) * SM::TW + (tile - SM::XB) * kTile;
+              *reinterpret_cast<uint4*>(s + n * 128 + at * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
+            if (MODE == 0 && lane == 0) mbar_arrive(&fixed[fixes & 1]);
+            ++fixes;
           }
-          if (MODE == 0) {
+          if (warp == 2) {
+            if (MODE == 0 && fix) {
+              if (!(ok = wait(&fixed[fixes & 1], (fixes >> 1) & 1))) break;
+              ++fixes;
+            }
+            // U = Σ_s (γ w_s) y_sᵀ, 16 tokens at a time
+            if (it > 0 && !(ok = wait(u_free, ph ^ 1))) break;
+#pragma unroll 1
+            for (int k = 0; k < kSteps; ++k) {
+              if (!(ok = wait(&ring_full[slot], ring_phase))) break;
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int part = 0; part < 3; ++part)
+                  mma_bf16_ts(tmem + kColU, tmem + kColRing + slot * 3 * kPart + part * kPart, dMN + sY + k * (kStep * 8),
+                              id_u, (k | part) != 0);
+                mma_commit(&ring_empty[slot]);
+                if (k == kSteps - 1) mma_commit(u_full);
+              }
+              __syncwarp();
+              if (++slot == kRing) {
+                slot = 0;
+                ring_phase ^= 1;
+              }
+            }
+            if (!ok) break;
+          } else if (MODE == 0) {
             // scores; P of the chunk before has been read
             if (it > 0 && !(ok = wait(o_full, ph ^ 1))) break;
+            if (!(ok = wait(&x_full[it % NX], (it / NX) & 1))) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -310,33 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
               mma_commit(mx_full);
             }
             __syncwarp();
-          }
-          // U = Σ_s (γ w_s) y_sᵀ, 16 tokens at a time
-          if (it > 0 && !(ok = wait(u_free, ph ^ 1))) break;
-#pragma unroll 1
-          for (int k = 0; k < kSteps; ++k) {
-            if (!(ok = wait(&ring_full[slot], ring_phase))) break;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-              for (int part = 0; part < 3; ++part)
-                mma_bf16_ts(tmem + kColU, tmem + kColRing + slot * 3 * kPart + part * kPart, dMN + sY + k * (kStep * 8), id_u,
-                            (k | part) != 0);
-              mma_commit(&ring_empty[slot]);
-            }
-            __syncwarp();
-            if (++slot == kRing) {
-              slot = 0;
-              ring_phase ^= 1;
-            }
-          }
-          if (!ok) break;
-          if (elect_one()) {
-            mma_commit(u_full);
-            if (MODE == 1) mma_commit(&empty[st]);
-          }
-          __syncwarp();
-          if (MODE == 0) {
+            if (!(ok = wait(&w_full[it % NW], (it / NW) & 1))) break;
             if (!(ok = wait(p_ready, ph))) break;
             tc_fence_after();
             if (elect_one()) {
@@ -350,35 +378,35 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         }
       }
       if (!ok) give_up(72);
-      // every MMA of the CTA has completed when `done` does
+      // every MMA of this warp has completed when its `done` does
       if (elect_one()) {
-        mma_commit(done);
+        mma_commit(&done[warp - 1]);
         const uint64_t w0 = globaltimer_ns();
-        while (!mbar_try_wait(done, 0) && globaltimer_ns() - w0 < kWaitLimitNs) {
+        while (!mbar_try_wait(&done[warp - 1], 0) && globaltimer_ns() - w0 < kWaitLimitNs) {
         }
       }
       __syncwarp();
-    } else if (warp == 2) {
+    } else if (MODE == 0) {
       // ---------------- stores ----------------
-      if (MODE == 0) {
+      {
         uint32_t it = 0;
         bool ok = true;
-        for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
+        for (uint32_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
           const LaItem t = la_item(p, item);
           for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
-            const int st = it % NS;
+            const int st = it % NW;
             int64_t t0;
             const int n = la_chunk(t, i, t0);
-            if (!(ok = wait(&staged[st], (it / NS) & 1))) break;
+            if (!(ok = wait(&staged[st], (it / NW) & 1))) break;
             if (elect_one()) {
               if (!t.r->out_f32 && (n == kLaChunk || t0 + n == p.L)) {
 #pragma unroll
                 for (int k = 0; k < SM::WB; ++k)
-                  tma_store_4d(&a.map[t.role][kMapOut], sm + st * SM::STAGE + SM::W + k * kTile, 64 * k, t.h, (int)t0, t.b);
+                  tma_store_4d(&a.map[t.role][kMapOut], sm + SM::W + st * SM::TW + k * kTile, 64 * k, t.h, (int)t0, t.b);
                 bulk_commit();
                 bulk_wait_read<0>();
               }
-              mbar_arrive(&empty[st]);
+              mbar_arrive(&w_empty[st]);
             }
             __syncwarp();
           }
@@ -387,35 +415,16 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         if (elect_one()) bulk_wait<0>();
         __syncwarp();
       }
-    } else {
-      // ---------------- an item's powers of γ ----------------
-      uint32_t ii = 0;
-      for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x, ++ii) {
-        const LaItem t = la_item(p, item);
-        if (!wait(&pw_empty[ii & 1], ((ii >> 1) & 1) ^ 1)) {
-          give_up(74);
-          break;
-        }
-        const float lg = p.g[t.h] * kLog2e;
-        const int rev = t.r->rev;
-        float* table = reinterpret_cast<float*>(sm + SM::POW) + (ii & 1) * kTable;
-        for (int e = lane; e < kTable; e += 32) {
-          const int d = rev ? kLaChunk - 1 - e : e - 32;
-          table[e] = d >= 0 ? la_pow(lg, d) : 0.f;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pw_full[ii & 1]);
-      }
     }
   } else if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (MODE == 0) {
       // ---------------- scores -> P ----------------
       const int wq = warp & 3, row = 32 * wq + lane;
       const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16) + kColP;
       uint32_t it = 0, ii = 0;
       bool ok = true;
-      for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x, ++ii) {
+      for (uint32_t item = blockIdx.x; item < a.items && ok; item += gridDim.x, ++ii) {
         const LaItem t = la_item(p, item);
         const int rev = t.r->rev;
         const uint32_t table = smem_u32(sm) + SM::POW + ((ii & 1) * kTable + la_origin(rev) + row) * 4;
@@ -424,6 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
           if (!(ok = wait(sc_full, it & 1))) break;
           tc_fence_after();
+          if (wq == 0 && lane == 0) mbar_arrive(&y_empty[it % NY]);
           // P's 32 tokens of block blk go to columns 16 blk .., which scores read earlier have left
 #pragma unroll 1
           for (int blk = 0; blk < 4; ++blk) {
@@ -454,25 +464,26 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       if (!ok) give_up(75);
     }
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (MODE == 0) {
       // ---------------- outputs ----------------
       const int wq = warp & 3, row = 32 * wq + lane;
       const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16) + kColO;
       uint32_t it = 0;
       bool ok = true;
-      for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
+      for (uint32_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
         const LaItem t = la_item(p, item);
         const LaRole& r = *t.r;
         const float lg = p.g[t.h] * kLog2e;
         for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
-          const int st = it % NS;
+          const int st = it % NW;
           const uint32_t ph = it & 1;
           int64_t t0;
           const int n = la_chunk(t, i, t0);
           const float f_in = r.s_inter * la_pow(lg, r.rev ? max(n - 1 - row, 0) : row + 1);
           if (!(ok = wait(mx_full, ph))) break;
           tc_fence_after();
+          if (wq == 0 && lane == 0) mbar_arrive(&x_empty[it % NX]);
 #pragma unroll 1
           for (int k = 0; k < DW / 32; ++k) {
             float f[32];
@@ -486,9 +497,10 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(p_ready);
+          if (!(ok = wait(&w_read[st], (it / NW) & 1))) break;
           if (!(ok = wait(o_full, ph))) break;
           tc_fence_after();
-          const uint32_t tile = smem_u32(sm) + st * SM::STAGE + SM::W;
+          const uint32_t tile = smem_u32(sm) + SM::W + st * SM::TW;
           const bool whole = !r.out_f32 && (n == kLaChunk || t0 + n == p.L);
           const int64_t at = t.b * r.out_sb + (t0 + row) * r.out_st + (int64_t)t.h * r.dw;
 #pragma unroll 1
@@ -530,14 +542,14 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       if (!ok) give_up(78);
     }
   } else if (warp < 16) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     // ---------------- the state ----------------
     const int wq = warp & 3, col = 32 * wq + lane;  // column of M = lane of U
     const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16);
     const bool active = col < DW;  // the same for a whole warp
     uint32_t it = 0;
     bool ok = true;
-    for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
+    for (uint32_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
       const LaItem t = la_item(p, item);
       const LaRole& r = *t.r;
       const float lg = p.g[t.h] * kLog2e, g_all = la_pow(lg, kLaChunk);
@@ -553,34 +565,34 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         for (int j = 0; j < DX; ++j)
           m[j] = (start != nullptr && j < r.dx && col < r.dw) ? start[(int64_t)j * sj + (int64_t)col * sc] : 0.f;
       }
-      // M's bf16 copy of 32 columns (the readout of the chunk before has taken the last one: its MMAs come
-      // before U's)
-      auto copy32 = [&](int k) {
+      // M's bf16 copy; the readout of the chunk before has taken the last one
+      auto copy = [&]() {
+        if (active) {
 #pragma unroll
-        for (int c = 4 * k; c < 4 * k + 4; ++c)
-          sts4(smem_u32(sm) + SM::M + (c >> 3) * (DW * 128) + swz16(col, c & 7), pair(m[8 * c], m[8 * c + 1]),
-               pair(m[8 * c + 2], m[8 * c + 3]), pair(m[8 * c + 4], m[8 * c + 5]), pair(m[8 * c + 6], m[8 * c + 7]));
-      };
-      auto copied = [&]() {
+          for (int c = 0; c < DX / 8; ++c)
+            sts4(smem_u32(sm) + SM::M + (c >> 3) * (DW * 128) + swz16(col, c & 7), pair(m[8 * c], m[8 * c + 1]),
+                 pair(m[8 * c + 2], m[8 * c + 3]), pair(m[8 * c + 4], m[8 * c + 5]), pair(m[8 * c + 6], m[8 * c + 7]));
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(m_ready);
       };
       const int chunks = t.c1 - t.c0;
-      if (MODE == 0 && chunks > 0) {
-        if (active) {
-#pragma unroll
-          for (int k = 0; k < DX / 32; ++k) copy32(k);
-        }
-        copied();
-      }
+#pragma unroll 1
       for (int i = 0; i < chunks; ++i, ++it) {
+        if (MODE == 0) {
+          if (it > 0 && !(ok = wait(mx_full, (it & 1) ^ 1))) break;
+          copy();
+        }
         int64_t t0;
         const int n = la_chunk(t, i, t0);
         const float g = n == kLaChunk ? g_all : la_pow(lg, n);
-        const bool more = MODE == 0 && i + 1 < chunks;
         if (!(ok = wait(u_full, it & 1))) break;
         tc_fence_after();
+        if (wq == 0 && lane == 0) {
+          mbar_arrive(&y_empty[it % NY]);
+          mbar_arrive(MODE == 0 ? &w_read[it % NW] : &w_empty[it % NW]);
+        }
         if (active) {
 #pragma unroll
           for (int k = 0; k < DX / 32; ++k) {
@@ -588,13 +600,11 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             tmem_ld32(tl + kColU + k * 32, f);
 #pragma unroll
             for (int j = 0; j < 32; ++j) m[k * 32 + j] = fmaf(g, m[k * 32 + j], f[j]);
-            if (more) copy32(k);
           }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(u_free);
-        if (more) copied();
       }
       if (!ok) break;
       if (col < r.dw && (MODE == 1 || (p.nseg == 1 && r.M_end != nullptr))) {
@@ -607,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     }
     if (!ok) give_up(76);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     // ---------------- (γ w)ᵀ ----------------
     const int wq = warp & 3;
     const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16);
@@ -618,25 +628,26 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       for (int k = 0; k < kRing * 3; ++k) tmem_st8(tl + kColRing + k * kPart, z);
       tmem_wait_st();
     }
-    uint32_t it = 0, ii = 0, slot = 0, ring_phase = 0;
+    uint32_t it = 0, ii = 0;
     bool ok = true;
-    for (int64_t item = blockIdx.x; item < a.items && ok; item += gridDim.x, ++ii) {
+    for (uint32_t item = blockIdx.x; item < a.items && ok; item += gridDim.x, ++ii) {
       const LaItem t = la_item(p, item);
       const int rev = t.r->rev;
       const uint32_t table = smem_u32(sm) + SM::POW + ((ii & 1) * kTable + la_origin(rev)) * 4;
       const float f_w = rev ? t.r->s_u * la_pow(p.g[t.h] * kLog2e, 1) : t.r->s_u;
       if (!(ok = wait(&pw_full[ii & 1], (ii >> 1) & 1))) break;
       for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
-        const int st = it % NS;
+        const int st = it % NW;
         int64_t t0;
         const int n = la_chunk(t, i, t0);
-        if (!(ok = wait(&full[st], (it / NS) & 1))) break;
+        if (!(ok = wait(&w_full[st], (it / NW) & 1))) break;
         // 16 tokens at a time: 8 x 8 blocks of W, transposed on the way to the registers, where thread t
         // holds channel t / 4 of tokens 2 (t % 4) + 0..1, scaled, split and stored in that form
-        const uint32_t tw = smem_u32(sm) + st * SM::STAGE + SM::W + (wq >> 1) * kTile + ((lane & 7) + 8 * (lane >> 4)) * 128;
+        const uint32_t tw = smem_u32(sm) + SM::W + st * SM::TW + (wq >> 1) * kTile + ((lane & 7) + 8 * (lane >> 4)) * 128;
 #pragma unroll 1
-        for (int k = 0; k < kSteps; ++k) {
-          if (!(ok = wait(&ring_empty[slot], ring_phase ^ 1))) break;
+        for (int k = (warp >> 2) & 1; k < kSteps; k += 2) {
+          const uint32_t step = it * kSteps + k, slot = step % kRing;
+          if (!(ok = wait(&ring_empty[slot], ((step / kRing) & 1) ^ 1))) break;
           tc_fence_after();
           if (active) {
             uint32_t raw[2][4];
@@ -677,10 +688,6 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&ring_full[slot]);
-          if (++slot == kRing) {
-            slot = 0;
-            ring_phase ^= 1;
-          }
         }
         if (!ok) break;
       }
@@ -732,7 +739,7 @@ cudaError_t launch_tc(const LaTcArgs& a, int sms, cudaStream_t s) {
   constexpr int smem = 1024 + LaSmem<DX, DW, MODE>::BYTES;
   const cudaError_t e = cudaFuncSetAttribute(la_tc_kernel<DX, DW, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  la_tc_kernel<DX, DW, MODE><<<(unsigned)std::min<int64_t>(a.items, sms), kThreads, smem, s>>>(a);
+  la_tc_kernel<DX, DW, MODE><<<(unsigned)std::min<uint32_t>(a.items, sms), kThreads, smem, s>>>(a);
   note_launch();
   return cudaGetLastError();
 }
@@ -743,7 +750,7 @@ cudaError_t launch_tc(const LaTcArgs& a, int sms, cudaStream_t s) {
 cudaError_t run_la_tc(const LaParams& p, bool states, cudaStream_t s) {
   LaTcArgs a;
   a.p = p;
-  a.items = (int64_t)p.n_roles * p.B * p.H * p.nseg;
+  a.items = (uint32_t)p.n_roles * p.B * p.H * p.nseg;  // below 2^30
   for (int i = 0; i < p.n_roles; ++i) {
     const LaRole& r = p.role[i];
     if (!la_map(&a.map[i][kMapX], r.x.p, r.dx, p.H / r.x.div, r.x.st, p.L, p.B) ||

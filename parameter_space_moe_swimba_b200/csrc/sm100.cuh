@@ -62,6 +62,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 __device__ __forceinline__ bool mbar_wait_close(uint64_t* bar, uint32_t parity, volatile int* abort) {
   uint64_t t0 = 0;
   for (;;) {
+#pragma unroll 1  // 64 copies of the poll at every wait would crowd the instruction cache
     for (int i = 0; i < 64; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
