@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
   const uint32_t tmem = *tmem_slot;
   // The whole warp waits and goes on, or gives up, together.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait_close(bar, parity, abort_flag));
+    return mbar_wait_warp(bar, parity, abort_flag);
   };
   auto give_up = [&](int where) {
     *abort_flag = 1;
