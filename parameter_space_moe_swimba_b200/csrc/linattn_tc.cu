@@ -14,20 +14,23 @@
 //                two and one of these MMAs, and few MMAs queue up: one warp for both made every wait
 //                a gap in the tensor cores' work.)
 //   warp 3       TMA stores of the finished output tiles
-//   warps 4-7    scores -> P: bf16, in place, the A operand of P W; one row i = TMEM lane each
-//   warps 8-11   the outputs' rows: the carried state's readout scaled in place, P W added to it by the
-//                MMA, the sum into the W tile, which no MMA reads any more, and from there to memory
+//   warps 4-11   one row i = TMEM lane each, two warps per row with half of its columns: scores -> P
+//                (bf16, in place, the A operand of P W); the carried state's readout scaled in place,
+//                to which the MMA adds P W; the sum into the W tile, which no MMA reads any more, and
+//                from there to memory
 //   warps 12-15  one column c of M each, in fp32 registers for the whole item: M's bf16 copy for the
 //                readout (the only rounding of M), M <- γ^n M + U. (U is summed apart from M: the tensor
 //                cores' own accumulation would lose a little of M at every step.)
 //   warps 16-23  (γ w)ᵀ as three bf16 parts into tensor memory (a ring of 16-token steps, dealt in turn to
 //                two sets of four warps)
-// Except for M's columns all loops stay rolled over blocks of 32 columns: five kinds of warps share the
-// instruction cache, and straight-line code ran at a quarter of an instruction per cycle and warp.
+// Except for M's columns all loops stay rolled: six kinds of warps share the instruction cache, whose misses
+// go to a cache that the SMs of a cluster share in their turn. With every loop unrolled, a chunk took a
+// quarter longer on SMs with 15 neighbours at work than on those with few.
 // Rounded to bf16: P and M's copy, once each, because each meets a bf16 operand and makes a bf16
 // output; γ w enters M as hi + mid + lo, 24 bits together, so that M stays an fp32 state (two parts
 // would put 3e-6 into S_final and dS0, three 1e-7).
-// Tensor memory: scores / P 128 columns, out 128, U dx, the γ w ring 120.
+// Tensor memory: scores / P 128 columns, out 128, U dx, the γ w ring 96.
+// P's tokens 0-63 lie in columns 0-31, tokens 64-127 in columns 64-95: where the same warp has read scores.
 // Every wait is bounded; a wait that runs out records SWIMBA_ERR_TIMEOUT, and the CTA drains and exits.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -45,9 +48,9 @@ namespace {
 
 constexpr int kTile = kLaChunk * 128;  // 128 tokens x 128 bytes (64 bf16), 128-byte swizzle: 16 KB
 constexpr int kThreads = 768;
-// γ w ring: 5 slots of 16 tokens (one MMA step) x 3 parts x 8 columns. Slots of 16 tokens rather than 32
+// γ w ring: 4 slots of 16 tokens (one MMA step) x 3 parts x 8 columns. Slots of 16 tokens rather than 32
 // let the warps that fill it refill a slot in half the time that its MMAs and theirs keep it busy.
-constexpr int kRing = 5, kPart = 8, kStep = 16, kSteps = kLaChunk / kStep;
+constexpr int kRing = 4, kPart = 8, kStep = 16, kSteps = kLaChunk / kStep;
 constexpr uint32_t kColP = 0, kColO = 128, kColU = 256, kColRing = 384;
 
 // An item's powers of γ by distance, with 32 zeros on the side that the mask hides: 0 .. 0 γ^0 .. γ^127, or
@@ -185,13 +188,13 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
   if (threadIdx.x == 0) {
     for (int i = 0; i < NX; ++i) mbar_init(&x_full[i], 1), mbar_init(&x_empty[i], 1);
     for (int i = 0; i < NY; ++i) mbar_init(&y_full[i], 1), mbar_init(&y_empty[i], MODE == 0 ? 2 : 1);
-    for (int i = 0; i < NW; ++i) mbar_init(&w_full[i], 1), mbar_init(&w_empty[i], 1), mbar_init(&staged[i], 4), mbar_init(&w_read[i], 1);
+    for (int i = 0; i < NW; ++i) mbar_init(&w_full[i], 1), mbar_init(&w_empty[i], 1), mbar_init(&staged[i], 8), mbar_init(&w_read[i], 1);
     mbar_init(sc_full, 1);
-    mbar_init(p_ready, 8);  // warps 4-7: P; warps 8-11: the readout's scaling
+    mbar_init(p_ready, 8);
     mbar_init(m_ready, 4);
     mbar_init(mx_full, 1);
     mbar_init(o_full, 1);
-    mbar_init(o_free, 4);
+    mbar_init(o_free, 8);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&ring_full[i], 4);
       mbar_init(&ring_empty[i], 1);
@@ -200,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     mbar_init(u_free, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&pw_full[i], 1);
-      mbar_init(&pw_empty[i], MODE == 0 ? 12 : 8);  // warps 4-7 (MODE 0) and 16-23
+      mbar_init(&pw_empty[i], MODE == 0 ? 16 : 8);  // warps 4-11 (MODE 0) and 16-23
     }
     mbar_init(&fixed[0], 1);
     mbar_init(&fixed[1], 1);
@@ -253,14 +256,14 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             for (int k = 0; k < boxes; ++k) tma_load_4d(sm + at + k * kTile, m, bar, 64 * k, t.h / div, (int)t0, t.b);
           };
           // in the order in which the tiles come free
+          if (!(ok = wait(&w_empty[it % NW], ((it / NW) & 1) ^ 1))) break;
+          if (elect_one()) load(SM::WB, SM::W + (it % NW) * SM::TW, &map[kMapW], &w_full[it % NW], t.r->w.div);
+          if (!(ok = wait(&y_empty[it % NY], ((it / NY) & 1) ^ 1))) break;
+          if (elect_one()) load(SM::XB, SM::Y + (it % NY) * SM::TY, &map[kMapY], &y_full[it % NY], t.r->y.div);
           if (MODE == 0) {
             if (!(ok = wait(&x_empty[it % NX], ((it / NX) & 1) ^ 1))) break;
             if (elect_one()) load(SM::XB, SM::X + (it % NX) * SM::TX, &map[kMapX], &x_full[it % NX], t.r->x.div);
           }
-          if (!(ok = wait(&y_empty[it % NY], ((it / NY) & 1) ^ 1))) break;
-          if (elect_one()) load(SM::XB, SM::Y + (it % NY) * SM::TY, &map[kMapY], &y_full[it % NY], t.r->y.div);
-          if (!(ok = wait(&w_empty[it % NW], ((it / NW) & 1) ^ 1))) break;
-          if (elect_one()) load(SM::WB, SM::W + (it % NW) * SM::TW, &map[kMapW], &w_full[it % NW], t.r->w.div);
           __syncwarp();
         }
       }
@@ -286,8 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       const uint32_t base = smem_u32(sm);
       // descriptors of address 0, to which a tile's address / 16 is added
       const uint64_t dK = smem_desc(0, 16, 1024, kLayoutSW128), dMN = smem_desc(0, kTile, 1024, kLayoutSW128);
-      auto kstep = [](int ks, int box) { return (uint32_t)((ks >> 2) * (box >> 4) + (ks & 3) * 2); };
-      uint32_t it = 0, slot = 0, ring_phase = 0, fixes = 0;
+      uint32_t it = 0, fixes = 0;
       bool ok = true;
       for (uint32_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
         const LaItem t = la_item(p, item);
@@ -323,21 +325,18 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             if (it > 0 && !(ok = wait(u_free, ph ^ 1))) break;
 #pragma unroll 1
             for (int k = 0; k < kSteps; ++k) {
-              if (!(ok = wait(&ring_full[slot], ring_phase))) break;
+              constexpr int R = kRing;
+              if (!(ok = wait(&ring_full[k % R], (it * (kSteps / R) + k / R) & 1))) break;
               tc_fence_after();
               if (elect_one()) {
 #pragma unroll
                 for (int part = 0; part < 3; ++part)
-                  mma_bf16_ts(tmem + kColU, tmem + kColRing + slot * 3 * kPart + part * kPart, dMN + sY + k * (kStep * 8),
+                  mma_bf16_ts(tmem + kColU, tmem + kColRing + (k % R) * 3 * kPart + part * kPart, dMN + sY + k * (kStep * 8),
                               id_u, (k | part) != 0);
-                mma_commit(&ring_empty[slot]);
+                mma_commit(&ring_empty[k % R]);
                 if (k == kSteps - 1) mma_commit(u_full);
               }
               __syncwarp();
-              if (++slot == kRing) {
-                slot = 0;
-                ring_phase ^= 1;
-              }
             }
             if (!ok) break;
           } else if (MODE == 0) {
@@ -346,9 +345,12 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             if (!(ok = wait(&x_full[it % NX], (it / NX) & 1))) break;
             tc_fence_after();
             if (elect_one()) {
+#pragma unroll 1
+              for (int box = 0; box < SM::XB; ++box)
 #pragma unroll
-              for (int ks = 0; ks < DX / 16; ++ks)
-                mma_bf16(tmem + kColP, dK + sX + kstep(ks, kTile), dK + sY + kstep(ks, kTile), id_sc, ks > 0);
+                for (int k = 0; k < 4; ++k)
+                  mma_bf16(tmem + kColP, dK + sX + box * (kTile >> 4) + k * 2, dK + sY + box * (kTile >> 4) + k * 2, id_sc,
+                           (box | k) != 0);
               mma_commit(sc_full);
             }
             __syncwarp();
@@ -357,10 +359,12 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             if (it > 0 && !(ok = wait(o_free, ph ^ 1))) break;
             tc_fence_after();
             if (elect_one()) {
+#pragma unroll 1
+              for (int box = 0; box < SM::XB; ++box)
 #pragma unroll
-              for (int ks = 0; ks < DX / 16; ++ks)
-                mma_bf16(tmem + kColO, dK + sX + kstep(ks, kTile), dK + ((base + SM::M) >> 4) + kstep(ks, DW * 128), id_mx,
-                         ks > 0);
+                for (int k = 0; k < 4; ++k)
+                  mma_bf16(tmem + kColO, dK + sX + box * (kTile >> 4) + k * 2,
+                           dK + ((base + SM::M) >> 4) + box * (DW * 128 >> 4) + k * 2, id_mx, (box | k) != 0);
               mma_commit(mx_full);
             }
             __syncwarp();
@@ -368,9 +372,11 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             if (!(ok = wait(p_ready, ph))) break;
             tc_fence_after();
             if (elect_one()) {
+#pragma unroll 1
+              for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int ks = 0; ks < kLaChunk / 16; ++ks)
-                mma_bf16_ts(tmem + kColO, tmem + kColP + ks * 8, dMN + sW + ks * 128, id_pw, 1u);
+                for (int k = 0; k < 4; ++k)
+                  mma_bf16_ts(tmem + kColO, tmem + kColP + h * 64 + k * 8, dMN + sW + (4 * h + k) * 128, id_pw, 1u);
               mma_commit(o_full);
             }
             __syncwarp();
@@ -416,31 +422,37 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         __syncwarp();
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (MODE == 0) {
-      // ---------------- scores -> P ----------------
-      const int wq = warp & 3, row = 32 * wq + lane;
-      const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16) + kColP;
+      // ---------------- scores -> P, outputs ----------------
+      const int wq = warp & 3, set = (warp >> 2) - 1, row = 32 * wq + lane;
+      const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16);
       uint32_t it = 0, ii = 0;
       bool ok = true;
       for (uint32_t item = blockIdx.x; item < a.items && ok; item += gridDim.x, ++ii) {
         const LaItem t = la_item(p, item);
-        const int rev = t.r->rev;
+        const LaRole& r = *t.r;
+        const int rev = r.rev;
         const uint32_t table = smem_u32(sm) + SM::POW + ((ii & 1) * kTable + la_origin(rev) + row) * 4;
-        const float s_intra = t.r->s_inter * t.r->s_u;
+        const float s_intra = r.s_inter * r.s_u, lg = p.g[t.h] * kLog2e;
+        const float f_all = r.s_inter * la_pow(lg, rev ? kLaChunk - 1 - row : row + 1);
         if (!(ok = wait(&pw_full[ii & 1], (ii >> 1) & 1))) break;
         for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
-          if (!(ok = wait(sc_full, it & 1))) break;
+          const int st = it % NW;
+          const uint32_t ph = it & 1;
+          int64_t t0;
+          const int n = la_chunk(t, i, t0);
+          if (!(ok = wait(sc_full, ph))) break;
           tc_fence_after();
-          if (wq == 0 && lane == 0) mbar_arrive(&y_empty[it % NY]);
-          // P's 32 tokens of block blk go to columns 16 blk .., which scores read earlier have left
+          if (warp == 4 && lane == 0) mbar_arrive(&y_empty[it % NY]);
+          // 32 tokens at a time: block blk's bf16 pairs go where this warp's first scores were
 #pragma unroll 1
-          for (int blk = 0; blk < 4; ++blk) {
+          for (int blk = 2 * set; blk < 2 * set + 2; ++blk) {
             uint32_t w16[16];
             if (rev ? blk >= wq : blk <= wq) {
               float f[32];
-              tmem_ld32(tl + blk * 32, f);
+              tmem_ld32(tl + kColP + blk * 32, f);
               const uint32_t at = table - blk * 128;
 #pragma unroll
               for (int j = 0; j < 32; ++j) f[j] *= s_intra * lds1(at - j * 4);
@@ -450,48 +462,21 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
 #pragma unroll
               for (int j = 0; j < 16; ++j) w16[j] = 0u;
             }
-            tmem_st16(tl + blk * 16, w16);
+            tmem_st16(tl + kColP + set * 64 + (blk & 1) * 16, w16);
           }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(p_ready);
-        }
-        if (!ok) break;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pw_empty[ii & 1]);
-      }
-      if (!ok) give_up(75);
-    }
-  } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (MODE == 0) {
-      // ---------------- outputs ----------------
-      const int wq = warp & 3, row = 32 * wq + lane;
-      const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16) + kColO;
-      uint32_t it = 0;
-      bool ok = true;
-      for (uint32_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
-        const LaItem t = la_item(p, item);
-        const LaRole& r = *t.r;
-        const float lg = p.g[t.h] * kLog2e;
-        for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
-          const int st = it % NW;
-          const uint32_t ph = it & 1;
-          int64_t t0;
-          const int n = la_chunk(t, i, t0);
-          const float f_in = r.s_inter * la_pow(lg, r.rev ? max(n - 1 - row, 0) : row + 1);
           if (!(ok = wait(mx_full, ph))) break;
           tc_fence_after();
-          if (wq == 0 && lane == 0) mbar_arrive(&x_empty[it % NX]);
+          if (warp == 4 && lane == 0) mbar_arrive(&x_empty[it % NX]);
+          const float f_in = rev && n < kLaChunk ? r.s_inter * la_pow(lg, max(n - 1 - row, 0)) : f_all;
+          const uint32_t to = tl + kColO + set * (DW / 2);
 #pragma unroll 1
-          for (int k = 0; k < DW / 32; ++k) {
+          for (int k = 0; k < DW / 64; ++k) {
             float f[32];
             uint32_t u[32];
-            tmem_ld32(tl + k * 32, f);
+            tmem_ld32(to + k * 32, f);
 #pragma unroll
             for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(f_in * f[j]);
-            tmem_st32(tl + k * 32, u);
+            tmem_st32(to + k * 32, u);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -504,18 +489,19 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           const bool whole = !r.out_f32 && (n == kLaChunk || t0 + n == p.L);
           const int64_t at = t.b * r.out_sb + (t0 + row) * r.out_st + (int64_t)t.h * r.dw;
 #pragma unroll 1
-          for (int k = 0; k < DW / 32; ++k) {
+          for (int k = 0; k < DW / 64; ++k) {
             float f[32];
-            tmem_ld32(tl + k * 32, f);
+            tmem_ld32(to + k * 32, f);
+            const int b32 = set * (DW / 64) + k;  // 32 columns of the tile
             if (whole) {
 #pragma unroll
               for (int c = 0; c < 4; ++c)
-                sts4(tile + (k >> 1) * kTile + swz16(row, (k & 1) * 4 + c), pair(f[8 * c], f[8 * c + 1]),
+                sts4(tile + (b32 >> 1) * kTile + swz16(row, (b32 & 1) * 4 + c), pair(f[8 * c], f[8 * c + 1]),
                      pair(f[8 * c + 2], f[8 * c + 3]), pair(f[8 * c + 4], f[8 * c + 5]), pair(f[8 * c + 6], f[8 * c + 7]));
             } else if (row < n) {
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
-                const int col = k * 32 + 8 * c;
+                const int col = b32 * 32 + 8 * c;
                 if (col >= r.dw) continue;
                 if (r.out_f32) {
                   float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(r.out) + at + col);
@@ -538,8 +524,11 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             mbar_arrive(&staged[st]);
           }
         }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pw_empty[ii & 1]);
       }
-      if (!ok) give_up(78);
+      if (!ok) give_up(75);
     }
   } else if (warp < 16) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
@@ -560,10 +549,15 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                              : p.nseg > 1  ? r.seg + (t.bh * p.nseg + t.seg) * size
                              : r.M0        ? r.M0 + t.bh * size
                                            : nullptr;
-        const int sj = p.nseg > 1 ? r.dw : r.sj, sc = p.nseg > 1 ? 1 : r.sc;
+        if (start != nullptr && col < r.dw) {
+          const int sj = p.nseg > 1 ? r.dw : r.sj;
+          const float* from = start + (int64_t)col * (p.nseg > 1 ? 1 : r.sc);
 #pragma unroll
-        for (int j = 0; j < DX; ++j)
-          m[j] = (start != nullptr && j < r.dx && col < r.dw) ? start[(int64_t)j * sj + (int64_t)col * sc] : 0.f;
+          for (int j = 0; j < DX; ++j, from += sj) m[j] = j < r.dx ? *from : 0.f;
+        } else {
+#pragma unroll
+          for (int j = 0; j < DX; ++j) m[j] = 0.f;
+        }
       }
       // M's bf16 copy; the readout of the chunk before has taken the last one
       auto copy = [&]() {
@@ -608,11 +602,12 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       }
       if (!ok) break;
       if (col < r.dw && (MODE == 1 || (p.nseg == 1 && r.M_end != nullptr))) {
-        float* end = MODE == 1 ? r.seg + (t.bh * p.nseg + t.seg) * size : r.M_end + t.bh * size;
-        const int ej = MODE == 1 ? r.dw : r.sj, ec = MODE == 1 ? 1 : r.sc;
+        float* end = (MODE == 1 ? r.seg + (t.bh * p.nseg + t.seg) * size : r.M_end + t.bh * size) +
+                     (int64_t)col * (MODE == 1 ? 1 : r.sc);
+        const int ej = MODE == 1 ? r.dw : r.sj;
 #pragma unroll
-        for (int j = 0; j < DX; ++j)
-          if (j < r.dx) end[(int64_t)j * ej + (int64_t)col * ec] = m[j];
+        for (int j = 0; j < DX; ++j, end += ej)
+          if (j < r.dx) *end = m[j];
       }
     }
     if (!ok) give_up(76);
@@ -646,8 +641,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         const uint32_t tw = smem_u32(sm) + SM::W + st * SM::TW + (wq >> 1) * kTile + ((lane & 7) + 8 * (lane >> 4)) * 128;
 #pragma unroll 1
         for (int k = (warp >> 2) & 1; k < kSteps; k += 2) {
-          const uint32_t step = it * kSteps + k, slot = step % kRing;
-          if (!(ok = wait(&ring_empty[slot], ((step / kRing) & 1) ^ 1))) break;
+          const uint32_t slot = k % kRing;
+          if (!(ok = wait(&ring_empty[slot], ((it * (kSteps / kRing) + k / kRing) & 1) ^ 1))) break;
           tc_fence_after();
           if (active) {
             uint32_t raw[2][4];

@@ -59,16 +59,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 
 // The same for a whole converged warp, which goes on or gives up together. One poll and vote of a completed
 // barrier take about 35 cycles, mbar_wait's per-thread loop about 170 even when nothing is left to wait
-// for. The global timer and the abort flag are read after every 64 polls.
+// for; and it is short, for kernels whose warps share the instruction cache with five other kinds.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (;;) {
-    if (__any_sync(0xffffffffu, *abort != 0 || globaltimer_ns() - t0 > kWaitLimitNs)) return false;
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  uint32_t polls = 0, t0 = 0;
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+    if ((++polls & 63u) != 0) continue;
+    const uint32_t now = (uint32_t)(globaltimer_ns() >> 16);  // units of 66 microseconds
+    if (t0 == 0) t0 = now;
+    if (__any_sync(0xffffffffu, *abort != 0 || now - t0 > (uint32_t)(kWaitLimitNs >> 16))) return false;
   }
+  return true;
 }
 
 // ---- TMA -----------------------------------------------------------------------------------------
