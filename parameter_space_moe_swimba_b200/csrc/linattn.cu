@@ -288,21 +288,21 @@ swimba_status check_la(const swimba_linattn_dims* d) {
 LaPlan la_plan(const swimba_linattn_dims* d, int roles, bool tc) {
   const int64_t nch = (d->seqlen + kLaChunk - 1) / kLaChunk, heads = d->batch * d->n_heads * roles;
   const int64_t slots = tc ? kSMs : 4 * kSMs;
-  LaPlan best{tc, 1, (int)nch};
+  LaPlan best{tc, 1, (int)nch, tc};
   double least = (double)((heads + slots - 1) / slots) * nch;
   for (int64_t n = 2; n <= std::min<int64_t>(nch, 64); ++n) {
     const int64_t cps = (nch + n - 1) / n, segs = (nch + cps - 1) / cps;
     const double t = (double)((heads * segs + slots - 1) / slots) * cps * 1.5 + 4;
     if (t < least) {
       least = t;
-      best = LaPlan{tc, (int)segs, (int)cps};
+      best = LaPlan{tc, (int)segs, (int)cps, false};
     }
   }
   return best;
 }
 
 struct LaLayout {
-  size_t seg[kLaMaxRoles], part_k, part_v, total;
+  size_t seg[kLaMaxRoles], part_k, part_v, flags, states, total;
 };
 
 bool la_use_tc(const swimba_linattn_dims* d) { return d->io_dtype == SWIMBA_BF16; }
@@ -320,6 +320,10 @@ LaLayout la_layout(const swimba_linattn_dims* d, const LaPlan& pl, int roles) {
   if (roles > 1 && d->n_kv_heads < d->n_heads) {
     l.part_k = take((size_t)d->batch * d->seqlen * d->n_heads * d->d_k * 4);
     l.part_v = take((size_t)d->batch * d->seqlen * d->n_heads * d->d_v * 4);
+  }
+  if (pl.cut) {
+    l.flags = take(kLaFlagBytes);
+    l.states = take(kLaHandBytes);
   }
   l.total = off;
   return l;
@@ -391,8 +395,13 @@ void launch_rows(void* out, int64_t st, const float* part, int group, int kv, in
   note_launch();
 }
 
-LaParams la_params(const swimba_linattn_dims* d, const LaPlan& pl, const float* g, const int32_t* lens, void* ws) {
+float* at(void* ws, size_t off) { return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + off); }
+
+LaParams la_params(const swimba_linattn_dims* d, const LaPlan& pl, const LaLayout& l, const float* g,
+                   const int32_t* lens, void* ws) {
   LaParams p{};
+  p.hand_flags = pl.cut ? reinterpret_cast<int*>(at(ws, l.flags)) : nullptr;
+  p.hand_states = pl.cut ? at(ws, l.states) : nullptr;
   p.g = g;
   p.lens = lens;
   p.L = d->seqlen;
@@ -405,8 +414,6 @@ LaParams la_params(const swimba_linattn_dims* d, const LaPlan& pl, const float* 
 }
 
 LaStream la_stream(const void* p, int64_t stride, int64_t L, int div) { return LaStream{p, stride, stride * L, div}; }
-
-float* at(void* ws, size_t off) { return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + off); }
 
 }  // namespace
 }  // namespace swimba
@@ -433,7 +440,7 @@ swimba_status swimba_linattn_fwd(const swimba_linattn_dims* dims, const void* q,
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(S0) || !aligned16(S_final) ||
       !aligned16(ws))
     return SWIMBA_ERR_ALIGN;
-  LaParams p = la_params(dims, pl, log_decay, lens, ws);
+  LaParams p = la_params(dims, pl, l, log_decay, lens, ws);
   const int group = dims->n_heads / dims->n_kv_heads;
   const int64_t L = dims->seqlen, ow = (int64_t)dims->n_heads * dims->d_v;
   p.n_roles = 1;
@@ -453,6 +460,7 @@ swimba_status swimba_linattn_fwd(const swimba_linattn_dims* dims, const void* q,
   r.sj = dims->d_v;
   r.sc = 1;
   r.seg = pl.nseg > 1 ? at(ws, l.seg[0]) : nullptr;
+  r.parts = S_final != nullptr ? 3 : 2;
   return api_cuda_status(run_roles(p, dims->io_dtype == SWIMBA_BF16, static_cast<cudaStream_t>(stream)));
 }
 
@@ -500,7 +508,7 @@ swimba_status swimba_linattn_bwd(const swimba_linattn_dims* dims, const void* q,
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(g_o) || !aligned16(dq) || !aligned16(dk) ||
       !aligned16(dv) || !aligned16(S0) || !aligned16(g_S) || !aligned16(dS0) || !aligned16(ws))
     return SWIMBA_ERR_ALIGN;
-  LaParams p = la_params(dims, pl, log_decay, lens, ws);
+  LaParams p = la_params(dims, pl, l, log_decay, lens, ws);
   const int H = dims->n_heads, group = H / dims->n_kv_heads, d_k = dims->d_k, d_v = dims->d_v;
   const int64_t L = dims->seqlen, ow = (int64_t)H * d_v;
   const LaStream sq = la_stream(q, dims->q_stride, L, 1), sk = la_stream(k, dims->k_stride, L, group),
@@ -522,6 +530,7 @@ swimba_status swimba_linattn_bwd(const swimba_linattn_dims* dims, const void* q,
     r.sj = i == 2 ? d_v : 1;
     r.sc = i == 2 ? 1 : d_v;
     r.seg = pl.nseg > 1 ? at(ws, l.seg[i]) : nullptr;
+    r.parts = r.M_end != nullptr ? 3 : 2;
     if (i > 0 && shared) {
       r.out = at(ws, i == 1 ? l.part_k : l.part_v);
       r.out_st = (int64_t)H * r.dw;

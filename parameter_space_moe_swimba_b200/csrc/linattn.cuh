@@ -36,6 +36,7 @@ struct LaRole {
   float* M_end;          // likewise
   int sj, sc;
   float* seg;            // [B H, nseg, dx, dw] segment states, or null (one segment)
+  int parts;             // bf16 parts of the weighted values: 3 where M itself is an output, else 2
 };
 
 struct LaParams {
@@ -46,6 +47,9 @@ struct LaParams {
   int64_t L;
   int B, H;
   int nseg, cps;         // segments per sequence, chunks per segment
+  int balanced;          // tensor cores: all chunks dealt to the CTAs in equal shares, cutting sequences
+  int* hand_flags;       // balanced: per CTA, zeroed before the launch
+  float* hand_states;    // balanced: per CTA, the state at the cut of the sequence it begins
   void* status;
 };
 
@@ -70,6 +74,11 @@ __device__ __forceinline__ void la_segment(const LaParams& p, int64_t len, int s
 struct LaPlan {
   bool tc;        // tensor-core kernel (bf16)
   int nseg, cps;  // segments per sequence, chunks per segment
+  bool cut;       // sequences may be cut between two CTAs (see run_la_tc): room for the states handed over
 };
+
+constexpr int kLaCtas = 148;  // one per SM
+constexpr size_t kLaHandBytes = (size_t)kLaCtas * 128 * 128 * 4;
+constexpr size_t kLaFlagBytes = 1024;
 
 }  // namespace swimba

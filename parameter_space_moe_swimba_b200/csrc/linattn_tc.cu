@@ -26,9 +26,15 @@
 // Except for M's columns all loops stay rolled: six kinds of warps share the instruction cache, whose misses
 // go to a cache that the SMs of a cluster share in their turn. With every loop unrolled, a chunk took a
 // quarter longer on SMs with 15 neighbours at work than on those with few.
+// Where there are as many sequences and heads as CTAs, all chunks are dealt to the CTAs in equal shares:
+// a CTA's share then begins and ends inside a sequence. It first does the beginning of the sequence that
+// its share ends in and hands the state over in global memory, then its whole sequences, and last the
+// rest of the sequence that its share begins in, whose state the CTA before it handed over at its start.
+// (256 sequences and heads on 148 CTAs: 56 chunks per CTA in place of 64.)
+//
 // Rounded to bf16: P and M's copy, once each, because each meets a bf16 operand and makes a bf16
-// output; γ w enters M as hi + mid + lo, 24 bits together, so that M stays an fp32 state (two parts
-// would put 3e-6 into S_final and dS0, three 1e-7).
+// output; γ w enters M as hi + mid + lo, 24 bits together, where M is an output, so that it stays an fp32
+// state (two parts would put 3e-6 into S_final and dS0, three 1e-7); else as hi + mid.
 // Tensor memory: scores / P 128 columns, out 128, U dx, the γ w ring 96.
 // P's tokens 0-63 lie in columns 0-31, tokens 64-127 in columns 64-95: where the same warp has read scores.
 // Every wait is bounded; a wait that runs out records SWIMBA_ERR_TIMEOUT, and the CTA drains and exits.
@@ -48,27 +54,33 @@ namespace {
 
 constexpr int kTile = kLaChunk * 128;  // 128 tokens x 128 bytes (64 bf16), 128-byte swizzle: 16 KB
 constexpr int kThreads = 768;
-// γ w ring: 4 slots of 16 tokens (one MMA step) x 3 parts x 8 columns. Slots of 16 tokens rather than 32
+// γ w ring: slots of 16 tokens (one MMA step) x 3 parts x 8 columns. Slots of 16 tokens rather than 32
 // let the warps that fill it refill a slot in half the time that its MMAs and theirs keep it busy.
-constexpr int kRing = 4, kPart = 8, kStep = 16, kSteps = kLaChunk / kStep;
-constexpr uint32_t kColP = 0, kColO = 128, kColU = 256, kColRing = 384;
+constexpr int kPart = 8, kStep = 16, kSteps = kLaChunk / kStep;
+constexpr uint32_t kColP = 0, kColO = 128;
 
 // An item's powers of γ by distance, with 32 zeros on the side that the mask hides: 0 .. 0 γ^0 .. γ^127, or
 // for a reverse role γ^127 .. γ^0 0 .. 0, so that row i's factor for token s is element la_origin + i - s.
 constexpr int kTable = 32 + kLaChunk;
 __host__ __device__ constexpr int la_origin(bool rev) { return rev ? kLaChunk - 1 : 32; }
 
-enum { kMapX, kMapY, kMapW, kMapOut };
-
 struct LaTcArgs {
   CUtensorMap map[kLaMaxRoles][4];
   LaParams p;
   uint32_t items;
+  uint32_t share, extra;  // balanced: chunks per CTA, and how many CTAs have one more
 };
+
+enum { kMapX, kMapY, kMapW, kMapOut };
+
 
 template <int DX, int DW, int MODE>
 struct LaSmem {
   static constexpr int XB = DX / 64, WB = DW / 64;
+  // Without scores and outputs there is room for two U and a longer ring, and the warps that would make
+  // them fill it too.
+  static constexpr int NU = MODE == 0 ? 1 : 2, RING = MODE == 0 ? 4 : 8, SETS = MODE == 0 ? 2 : 4;
+  static constexpr uint32_t COL_U = MODE == 0 ? 256 : 0, COL_RING = MODE == 0 ? 384 : 256;
   static constexpr int TX = MODE == 0 ? XB * kTile : 0, TY = XB * kTile, TW = WB * kTile;  // one tile of each
   static constexpr int COPY = MODE == 0 ? DX * DW * 2 : 0;  // M's bf16 copy, [dw rows][dx], K-major
   // Tiles in flight. An X tile is free after two MMAs, a Y tile after U, a W tile only when the outputs
@@ -77,7 +89,7 @@ struct LaSmem {
   static constexpr int X = 0, Y = NX * TX, W = Y + NY * TY, M = W + NW * TW;
   static constexpr int POW = M + COPY;              // 2 x kTable floats
   static constexpr int BAR = POW + 2 * kTable * 4;  // barriers
-  static constexpr int NBAR = 2 * NX + 2 * NY + 4 * NW + 6 + 2 * kRing + 2 + 4 + 2 + 2;
+  static constexpr int NBAR = 2 * NX + 2 * NY + 4 * NW + 6 + 2 * RING + 2 * NU + 4 + 2 + 2;
   static constexpr int MISC = BAR + NBAR * 8;
   static constexpr int BYTES = MISC + 16;
   static_assert(BYTES + 1024 <= 232448, "shared memory of one CTA");
@@ -121,14 +133,40 @@ __device__ __forceinline__ uint32_t high_halves(float a, float b) {
 }
 __device__ __forceinline__ float top_bits(float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); }
 
+// A piece of one sequence and head (of one role): chunks [c0, c1) in natural order.
 struct LaItem {
-  const LaRole* r;
-  int role, b, h, seg, c0, c1;
+  const LaRole* r;  // in the kernel's parameters: what a chunk's loop uses is copied out first, since behind
+                    // every asm statement it would be loaded again, through memory
+  int role, b, h, seg, c0, c1, rev, parts;
   int64_t bh, len;
+  bool begins, ends;  // the state before it is given (else handed over); the state after it is the end's (else to be handed over)
 };
 
-__device__ __forceinline__ LaItem la_item(const LaParams& p, uint32_t item) {
-  LaItem t;
+// The k-th piece of this CTA.
+__device__ __forceinline__ bool la_item(const LaTcArgs& a, uint32_t k, LaItem& t) {
+  const LaParams& p = a.p;
+  uint32_t item, p0 = 0, p1 = 0xffffffffu;
+  if (!p.balanced) {
+    item = blockIdx.x + k * gridDim.x;
+    if (item >= a.items) return false;
+  } else {
+    const uint32_t nch = (uint32_t)p.cps;
+    const uint32_t g0 = blockIdx.x * a.share + min(blockIdx.x, a.extra),
+                   g1 = g0 + a.share + (blockIdx.x < a.extra ? 1u : 0u);
+    const uint32_t first = g0 / nch, r0 = g0 - first * nch, last = g1 / nch, r1 = g1 - last * nch;
+    const uint32_t whole0 = first + (r0 != 0), head = r1 != 0;
+    if (head && k == 0) {  // the beginning of the sequence that the share ends in
+      item = last;
+      p1 = r1;
+    } else if (k - head < last - whole0) {
+      item = whole0 + (k - head);
+    } else if (r0 != 0 && k - head == last - whole0) {  // the rest of the one that it begins in
+      item = first;
+      p0 = r0;
+    } else {
+      return false;
+    }
+  }
   const uint32_t rest = item / (uint32_t)p.n_roles, bh = rest / (uint32_t)p.nseg;
   t.role = (int)(item - rest * p.n_roles);
   t.seg = (int)(rest - bh * p.nseg);
@@ -136,14 +174,37 @@ __device__ __forceinline__ LaItem la_item(const LaParams& p, uint32_t item) {
   t.r = &p.role[t.role];
   t.b = (int)(bh / (uint32_t)p.H);
   t.h = (int)bh - t.b * p.H;
+  t.rev = t.r->rev;
+  t.parts = t.r->parts;
   t.len = la_len(p, t.b);
-  la_segment(p, t.len, t.seg, t.r->rev, t.c0, t.c1);
-  return t;
+  la_segment(p, t.len, t.seg, t.rev, t.c0, t.c1);
+  t.begins = p0 == 0;
+  t.ends = p1 == 0xffffffffu;
+  const int n = t.c1 - t.c0, a0 = (int)p0, a1 = t.ends ? n : (int)p1;
+  t.c1 = t.c0 + (t.rev ? n - a0 : a1);
+  t.c0 = t.c0 + (t.rev ? n - a1 : a0);
+  return true;
 }
 
+// A state handed from one CTA to the next through global memory: the four warps that write it each add 1 to
+// the flag, those that take it wait for 4. The writer has begun with this state, before anything that
+// waits, and runs: CTAs start in the order of their indices. The wait is bounded all the same.
+__device__ __forceinline__ void hand_over(int* flag, int lane) {
+  __threadfence();
+  __syncwarp();
+  if (lane == 0) atomicAdd(flag, 1);
+}
+__device__ __forceinline__ bool hand_wait(int* flag, volatile int* abort, int lane) {
+  const uint64_t t0 = globaltimer_ns();
+  while (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(flag) != 4)) {
+    if (__any_sync(0xffffffffu, *abort != 0 || globaltimer_ns() - t0 > kWaitLimitNs)) return false;
+  }
+  __threadfence();
+  return true;
+}
 // First token of the item's chunk number `i` and its count.
 __device__ __forceinline__ int la_chunk(const LaItem& t, int i, int64_t& t0) {
-  t0 = (int64_t)(t.r->rev ? t.c1 - 1 - i : t.c0 + i) * kLaChunk;
+  t0 = (int64_t)(t.rev ? t.c1 - 1 - i : t.c0 + i) * kLaChunk;
   return (int)min((int64_t)kLaChunk, t.len - t0);
 }
 
@@ -171,11 +232,11 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
   uint64_t* mx_full = m_ready + 1;                             // the readout in tensor memory; X and the copy free
   uint64_t* o_full = mx_full + 1;                              // P W in tensor memory, P and the tiles free
   uint64_t* o_free = o_full + 1;                               // out columns read
-  uint64_t* ring_full = o_free + 1;                            // [kRing]
-  uint64_t* ring_empty = ring_full + kRing;                    // [kRing]
-  uint64_t* u_full = ring_empty + kRing;
-  uint64_t* u_free = u_full + 1;                               // U read
-  uint64_t* pw_full = u_free + 1;                              // [2]
+  uint64_t* ring_full = o_free + 1;                            // [RING]
+  uint64_t* ring_empty = ring_full + SM::RING;                 // [RING]
+  uint64_t* u_full = ring_empty + SM::RING;                    // [NU]
+  uint64_t* u_free = u_full + SM::NU;                          // [NU] U read
+  uint64_t* pw_full = u_free + SM::NU;                              // [2]
   uint64_t* pw_empty = pw_full + 2;                            // [2]
   // [2] zeros behind a sequence's end written, in turn: warp 1 can be two such chunks ahead of warp 2's wait
   uint64_t* fixed = pw_empty + 2;
@@ -195,15 +256,17 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     mbar_init(mx_full, 1);
     mbar_init(o_full, 1);
     mbar_init(o_free, 8);
-    for (int i = 0; i < kRing; ++i) {
+    for (int i = 0; i < SM::RING; ++i) {
       mbar_init(&ring_full[i], 4);
       mbar_init(&ring_empty[i], 1);
     }
-    mbar_init(u_full, 1);
-    mbar_init(u_free, 4);
+    for (int i = 0; i < SM::NU; ++i) {
+      mbar_init(&u_full[i], 1);
+      mbar_init(&u_free[i], 4);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&pw_full[i], 1);
-      mbar_init(&pw_empty[i], MODE == 0 ? 16 : 8);  // warps 4-11 (MODE 0) and 16-23
+      mbar_init(&pw_empty[i], 16);  // warps 4-11 and 16-23
     }
     mbar_init(&fixed[0], 1);
     mbar_init(&fixed[1], 1);
@@ -234,15 +297,15 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       // ---------------- loads ----------------
       uint32_t it = 0, ii = 0;
       bool ok = true;
-      for (uint32_t item = blockIdx.x; item < a.items && ok; item += gridDim.x, ++ii) {
-        const LaItem t = la_item(p, item);
+      for (LaItem t; ok && la_item(a, ii, t); ++ii) {
         const CUtensorMap* map = a.map[t.role];
+        const int hx = t.h / t.r->x.div, hy = t.h / t.r->y.div, hw = t.h / t.r->w.div;
         if (!(ok = wait(&pw_empty[ii & 1], ((ii >> 1) & 1) ^ 1))) break;
         {
           const float lg = p.g[t.h] * kLog2e;
           float* table = reinterpret_cast<float*>(sm + SM::POW) + (ii & 1) * kTable;
           for (int e = lane; e < kTable; e += 32) {
-            const int d = t.r->rev ? kLaChunk - 1 - e : e - 32;
+            const int d = t.rev ? kLaChunk - 1 - e : e - 32;
             table[e] = d >= 0 ? la_pow(lg, d) : 0.f;
           }
           __syncwarp();
@@ -251,18 +314,18 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
           int64_t t0;
           la_chunk(t, i, t0);
-          auto load = [&](int boxes, int at, const CUtensorMap* m, uint64_t* bar, int div) {
+          auto load = [&](int boxes, int at, const CUtensorMap* m, uint64_t* bar, int head) {
             mbar_arrive_expect_tx(bar, boxes * kTile);
-            for (int k = 0; k < boxes; ++k) tma_load_4d(sm + at + k * kTile, m, bar, 64 * k, t.h / div, (int)t0, t.b);
+            for (int k = 0; k < boxes; ++k) tma_load_4d(sm + at + k * kTile, m, bar, 64 * k, head, (int)t0, t.b);
           };
           // in the order in which the tiles come free
           if (!(ok = wait(&w_empty[it % NW], ((it / NW) & 1) ^ 1))) break;
-          if (elect_one()) load(SM::WB, SM::W + (it % NW) * SM::TW, &map[kMapW], &w_full[it % NW], t.r->w.div);
+          if (elect_one()) load(SM::WB, SM::W + (it % NW) * SM::TW, &map[kMapW], &w_full[it % NW], hw);
           if (!(ok = wait(&y_empty[it % NY], ((it / NY) & 1) ^ 1))) break;
-          if (elect_one()) load(SM::XB, SM::Y + (it % NY) * SM::TY, &map[kMapY], &y_full[it % NY], t.r->y.div);
+          if (elect_one()) load(SM::XB, SM::Y + (it % NY) * SM::TY, &map[kMapY], &y_full[it % NY], hy);
           if (MODE == 0) {
             if (!(ok = wait(&x_empty[it % NX], ((it / NX) & 1) ^ 1))) break;
-            if (elect_one()) load(SM::XB, SM::X + (it % NX) * SM::TX, &map[kMapX], &x_full[it % NX], t.r->x.div);
+            if (elect_one()) load(SM::XB, SM::X + (it % NX) * SM::TX, &map[kMapX], &x_full[it % NX], hx);
           }
           __syncwarp();
         }
@@ -289,10 +352,9 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       const uint32_t base = smem_u32(sm);
       // descriptors of address 0, to which a tile's address / 16 is added
       const uint64_t dK = smem_desc(0, 16, 1024, kLayoutSW128), dMN = smem_desc(0, kTile, 1024, kLayoutSW128);
-      uint32_t it = 0, fixes = 0;
+      uint32_t it = 0, ii = 0, fixes = 0;
       bool ok = true;
-      for (uint32_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
-        const LaItem t = la_item(p, item);
+      for (LaItem t; ok && la_item(a, ii, t); ++ii) {
         for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
           const uint32_t ph = it & 1;
           int64_t t0;
@@ -322,19 +384,26 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
               ++fixes;
             }
             // U = Σ_s (γ w_s) y_sᵀ, 16 tokens at a time
-            if (it > 0 && !(ok = wait(u_free, ph ^ 1))) break;
+            const uint32_t ub = it % SM::NU, up = (it / SM::NU) & 1;
+            if (!(ok = wait(&u_free[ub], up ^ 1))) break;
+            // A poll queues up behind the MMAs issued before it; asked for after them, it left the tensor cores
+            // about 140 cycles without work at every step. So each step's is issued before the MMAs of the
+            // step before, and its answer is looked at after them.
+            constexpr int R = SM::RING;
+            bool here = mbar_try_wait(&ring_full[0], (it * (kSteps / R)) & 1);
 #pragma unroll 1
             for (int k = 0; k < kSteps; ++k) {
-              constexpr int R = kRing;
-              if (!(ok = wait(&ring_full[k % R], (it * (kSteps / R) + k / R) & 1))) break;
+              if (!__all_sync(0xffffffffu, here) && !(ok = wait(&ring_full[k % R], (it * (kSteps / R) + k / R) & 1))) break;
               tc_fence_after();
+              here = k + 1 < kSteps && mbar_try_wait(&ring_full[(k + 1) % R], (it * (kSteps / R) + (k + 1) / R) & 1);
               if (elect_one()) {
 #pragma unroll
                 for (int part = 0; part < 3; ++part)
-                  mma_bf16_ts(tmem + kColU, tmem + kColRing + (k % R) * 3 * kPart + part * kPart, dMN + sY + k * (kStep * 8),
-                              id_u, (k | part) != 0);
+                  if (part < 2 || t.parts == 3)
+                    mma_bf16_ts(tmem + SM::COL_U + ub * 128, tmem + SM::COL_RING + (k % R) * 3 * kPart + part * kPart,
+                                dMN + sY + k * (kStep * 8), id_u, (k | part) != 0);
                 mma_commit(&ring_empty[k % R]);
-                if (k == kSteps - 1) mma_commit(u_full);
+                if (k == kSteps - 1) mma_commit(&u_full[ub]);
               }
               __syncwarp();
             }
@@ -395,17 +464,17 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     } else if (MODE == 0) {
       // ---------------- stores ----------------
       {
-        uint32_t it = 0;
+        uint32_t it = 0, ii = 0;
         bool ok = true;
-        for (uint32_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
-          const LaItem t = la_item(p, item);
+        for (LaItem t; ok && la_item(a, ii, t); ++ii) {
+          const bool out_f32 = t.r->out_f32 != 0;
           for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
             const int st = it % NW;
             int64_t t0;
             const int n = la_chunk(t, i, t0);
             if (!(ok = wait(&staged[st], (it / NW) & 1))) break;
             if (elect_one()) {
-              if (!t.r->out_f32 && (n == kLaChunk || t0 + n == p.L)) {
+              if (!out_f32 && (n == kLaChunk || t0 + n == p.L)) {
 #pragma unroll
                 for (int k = 0; k < SM::WB; ++k)
                   tma_store_4d(&a.map[t.role][kMapOut], sm + SM::W + st * SM::TW + k * kTile, 64 * k, t.h, (int)t0, t.b);
@@ -422,21 +491,23 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         __syncwarp();
       }
     }
-  } else if (warp < 12) {
+  } else if (MODE == 0 && warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (MODE == 0) {
+    {
       // ---------------- scores -> P, outputs ----------------
       const int wq = warp & 3, set = (warp >> 2) - 1, row = 32 * wq + lane;
       const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16);
       uint32_t it = 0, ii = 0;
       bool ok = true;
-      for (uint32_t item = blockIdx.x; item < a.items && ok; item += gridDim.x, ++ii) {
-        const LaItem t = la_item(p, item);
+      for (LaItem t; ok && la_item(a, ii, t); ++ii) {
         const LaRole& r = *t.r;
-        const int rev = r.rev;
+        const int rev = t.rev;
         const uint32_t table = smem_u32(sm) + SM::POW + ((ii & 1) * kTable + la_origin(rev) + row) * 4;
-        const float s_intra = r.s_inter * r.s_u, lg = p.g[t.h] * kLog2e;
-        const float f_all = r.s_inter * la_pow(lg, rev ? kLaChunk - 1 - row : row + 1);
+        const float s_inter = r.s_inter, s_intra = s_inter * r.s_u, lg = p.g[t.h] * kLog2e;
+        const int out_f32 = r.out_f32, dw = r.dw;
+        const int64_t out_st = r.out_st, out_bh = t.b * r.out_sb + (int64_t)t.h * dw;
+        void* const out = r.out;
+        const float f_all = s_inter * la_pow(lg, rev ? kLaChunk - 1 - row : row + 1);
         if (!(ok = wait(&pw_full[ii & 1], (ii >> 1) & 1))) break;
         for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
           const int st = it % NW;
@@ -467,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           if (!(ok = wait(mx_full, ph))) break;
           tc_fence_after();
           if (warp == 4 && lane == 0) mbar_arrive(&x_empty[it % NX]);
-          const float f_in = rev && n < kLaChunk ? r.s_inter * la_pow(lg, max(n - 1 - row, 0)) : f_all;
+          const float f_in = rev && n < kLaChunk ? s_inter * la_pow(lg, max(n - 1 - row, 0)) : f_all;
           const uint32_t to = tl + kColO + set * (DW / 2);
 #pragma unroll 1
           for (int k = 0; k < DW / 64; ++k) {
@@ -486,8 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           if (!(ok = wait(o_full, ph))) break;
           tc_fence_after();
           const uint32_t tile = smem_u32(sm) + SM::W + st * SM::TW;
-          const bool whole = !r.out_f32 && (n == kLaChunk || t0 + n == p.L);
-          const int64_t at = t.b * r.out_sb + (t0 + row) * r.out_st + (int64_t)t.h * r.dw;
+          const bool whole = !out_f32 && (n == kLaChunk || t0 + n == p.L);
+          const int64_t at = out_bh + (t0 + row) * out_st;
 #pragma unroll 1
           for (int k = 0; k < DW / 64; ++k) {
             float f[32];
@@ -502,13 +573,13 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 const int col = b32 * 32 + 8 * c;
-                if (col >= r.dw) continue;
-                if (r.out_f32) {
-                  float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(r.out) + at + col);
+                if (col >= dw) continue;
+                if (out_f32) {
+                  float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + at + col);
                   dst[0] = make_float4(f[8 * c], f[8 * c + 1], f[8 * c + 2], f[8 * c + 3]);
                   dst[1] = make_float4(f[8 * c + 4], f[8 * c + 5], f[8 * c + 6], f[8 * c + 7]);
                 } else {
-                  *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(r.out) + at + col) =
+                  *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(out) + at + col) =
                       make_uint4(pair(f[8 * c], f[8 * c + 1]), pair(f[8 * c + 2], f[8 * c + 3]),
                                  pair(f[8 * c + 4], f[8 * c + 5]), pair(f[8 * c + 6], f[8 * c + 7]));
                 }
@@ -530,30 +601,33 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       }
       if (!ok) give_up(75);
     }
-  } else if (warp < 16) {
+  } else if (warp >= 12 && warp < 16) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     // ---------------- the state ----------------
     const int wq = warp & 3, col = 32 * wq + lane;  // column of M = lane of U
     const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16);
     const bool active = col < DW;  // the same for a whole warp
-    uint32_t it = 0;
+    uint32_t it = 0, ii = 0;
     bool ok = true;
-    for (uint32_t item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
-      const LaItem t = la_item(p, item);
+    for (LaItem t; ok && la_item(a, ii, t); ++ii) {
       const LaRole& r = *t.r;
       const float lg = p.g[t.h] * kLog2e, g_all = la_pow(lg, kLaChunk);
-      const int64_t size = (int64_t)r.dx * r.dw;
+      const int dx = r.dx, dw = r.dw;
+      const int64_t size = (int64_t)dx * dw;
       float m[DX];
       {
         const float* start = MODE == 1     ? nullptr
+                             : !t.begins   ? p.hand_states + (size_t)(blockIdx.x - 1) * 128 * 128
                              : p.nseg > 1  ? r.seg + (t.bh * p.nseg + t.seg) * size
                              : r.M0        ? r.M0 + t.bh * size
                                            : nullptr;
-        if (start != nullptr && col < r.dw) {
-          const int sj = p.nseg > 1 ? r.dw : r.sj;
-          const float* from = start + (int64_t)col * (p.nseg > 1 ? 1 : r.sc);
+        const bool own = t.begins && p.nseg == 1;  // in the caller's layout, else [dx, dw]
+        if (!t.begins && !(ok = hand_wait(&p.hand_flags[blockIdx.x - 1], abort_flag, lane))) break;
+        if (start != nullptr && col < dw) {
+          const int sj = own ? r.sj : dw;
+          const float* from = start + (int64_t)col * (own ? r.sc : 1);
 #pragma unroll
-          for (int j = 0; j < DX; ++j, from += sj) m[j] = j < r.dx ? *from : 0.f;
+          for (int j = 0; j < DX; ++j, from += sj) m[j] = j < dx ? __ldcg(from) : 0.f;
         } else {
 #pragma unroll
           for (int j = 0; j < DX; ++j) m[j] = 0.f;
@@ -581,7 +655,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         int64_t t0;
         const int n = la_chunk(t, i, t0);
         const float g = n == kLaChunk ? g_all : la_pow(lg, n);
-        if (!(ok = wait(u_full, it & 1))) break;
+        const uint32_t ub = it % SM::NU;
+        if (!(ok = wait(&u_full[ub], (it / SM::NU) & 1))) break;
         tc_fence_after();
         if (wq == 0 && lane == 0) {
           mbar_arrive(&y_empty[it % NY]);
@@ -591,24 +666,30 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
 #pragma unroll
           for (int k = 0; k < DX / 32; ++k) {
             float f[32];
-            tmem_ld32(tl + kColU + k * 32, f);
+            tmem_ld32(tl + SM::COL_U + ub * 128 + k * 32, f);
 #pragma unroll
             for (int j = 0; j < 32; ++j) m[k * 32 + j] = fmaf(g, m[k * 32 + j], f[j]);
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(u_free);
+        if (lane == 0) mbar_arrive(&u_free[ub]);
       }
       if (!ok) break;
-      if (col < r.dw && (MODE == 1 || (p.nseg == 1 && r.M_end != nullptr))) {
-        float* end = (MODE == 1 ? r.seg + (t.bh * p.nseg + t.seg) * size : r.M_end + t.bh * size) +
-                     (int64_t)col * (MODE == 1 ? 1 : r.sc);
-        const int ej = MODE == 1 ? r.dw : r.sj;
+      const bool hand = MODE == 0 && !t.ends;
+      float* end = MODE == 1                              ? r.seg + (t.bh * p.nseg + t.seg) * size
+                   : hand                                 ? p.hand_states + (size_t)blockIdx.x * 128 * 128
+                   : p.nseg == 1 && r.M_end != nullptr    ? r.M_end + t.bh * size
+                                                          : nullptr;
+      if (end != nullptr && col < dw) {
+        const bool own = MODE == 0 && !hand;
+        const int ej = own ? r.sj : dw;
+        end += (int64_t)col * (own ? r.sc : 1);
 #pragma unroll
         for (int j = 0; j < DX; ++j, end += ej)
-          if (j < r.dx) *end = m[j];
+          if (j < dx) *end = m[j];
       }
+      if (hand) hand_over(&p.hand_flags[blockIdx.x], lane);
     }
     if (!ok) give_up(76);
   } else {
@@ -617,17 +698,17 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     const int wq = warp & 3;
     const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16);
     const bool active = 32 * wq < DW;
+    const int set = warp >= 16 ? (warp >> 2) - 4 : (warp >> 2) + 1;  // 16-19, 20-23, then 4-7, 8-11
     if (!active) {  // those rows stay zero
       const uint32_t z[8] = {};
 #pragma unroll 1
-      for (int k = 0; k < kRing * 3; ++k) tmem_st8(tl + kColRing + k * kPart, z);
+      for (int k = 0; k < SM::RING * 3; ++k) tmem_st8(tl + SM::COL_RING + k * kPart, z);
       tmem_wait_st();
     }
     uint32_t it = 0, ii = 0;
     bool ok = true;
-    for (uint32_t item = blockIdx.x; item < a.items && ok; item += gridDim.x, ++ii) {
-      const LaItem t = la_item(p, item);
-      const int rev = t.r->rev;
+    for (LaItem t; ok && la_item(a, ii, t); ++ii) {
+      const int rev = t.rev;
       const uint32_t table = smem_u32(sm) + SM::POW + ((ii & 1) * kTable + la_origin(rev)) * 4;
       const float f_w = rev ? t.r->s_u * la_pow(p.g[t.h] * kLog2e, 1) : t.r->s_u;
       if (!(ok = wait(&pw_full[ii & 1], (ii >> 1) & 1))) break;
@@ -640,9 +721,10 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         // holds channel t / 4 of tokens 2 (t % 4) + 0..1, scaled, split and stored in that form
         const uint32_t tw = smem_u32(sm) + SM::W + st * SM::TW + (wq >> 1) * kTile + ((lane & 7) + 8 * (lane >> 4)) * 128;
 #pragma unroll 1
-        for (int k = (warp >> 2) & 1; k < kSteps; k += 2) {
-          const uint32_t slot = k % kRing;
-          if (!(ok = wait(&ring_empty[slot], ((it * (kSteps / kRing) + k / kRing) & 1) ^ 1))) break;
+        for (int k = set; k < kSteps; k += SM::SETS) {
+          constexpr int R = SM::RING;
+          const uint32_t slot = k % R;
+          if (!(ok = wait(&ring_empty[slot], ((it * (kSteps / R) + k / R) & 1) ^ 1))) break;
           tc_fence_after();
           if (active) {
             uint32_t raw[2][4];
@@ -673,10 +755,10 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                 mid[d] = high_halves(r0, r1);
                 lo[d] = high_halves(r0 - top_bits(r0), r1 - top_bits(r1));
               }
-              const uint32_t at = tl + ((uint32_t)(16 * half) << 16) + kColRing + slot * 3 * kPart;
+              const uint32_t at = tl + ((uint32_t)(16 * half) << 16) + SM::COL_RING + slot * 3 * kPart;
               tmem_st_16x128b_x2(at, hi);
               tmem_st_16x128b_x2(at + kPart, mid);
-              tmem_st_16x128b_x2(at + 2 * kPart, lo);
+              if (t.parts == 3) tmem_st_16x128b_x2(at + 2 * kPart, lo);
             }
             tmem_wait_st();
           }
@@ -754,9 +836,22 @@ cudaError_t run_la_tc(const LaParams& p, bool states, cudaStream_t s) {
         (!r.out_f32 && !la_map(&a.map[i][kMapOut], r.out, r.dw, p.H, r.out_st, p.L, p.B)))
       return cudaErrorInvalidValue;
   }
-  int dev = 0, sms = 148;
+  int dev = 0, sms = kLaCtas;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  sms = std::min(sms, kLaCtas);
+  // Equal shares cut sequences; they pay where whole ones would leave CTAs idle in the last round, and
+  // need at least as many pieces as CTAs, so that a sequence spans two shares at most. With lengths on
+  // the device the host does not know the shares.
+  const uint64_t total = (uint64_t)a.items * p.cps, rounds = (a.items + sms - 1) / sms;
+  a.share = (uint32_t)(total / sms);
+  a.extra = (uint32_t)(total % sms);
+  a.p.balanced = !states && p.hand_flags != nullptr && p.nseg == 1 && p.lens == nullptr && a.items >= (uint32_t)sms &&
+                 total < (1u << 31) && rounds * p.cps > total / sms + 3;
+  if (a.p.balanced) {
+    const cudaError_t e = cudaMemsetAsync(p.hand_flags, 0, kLaFlagBytes, s);
+    if (e != cudaSuccess) return e;
+  }
   const bool x64 = p.role[0].dx <= 64, w64 = p.role[0].dw <= 64;
   if (states)
     return x64 ? (w64 ? launch_tc<64, 64, 1>(a, sms, s) : launch_tc<64, 128, 1>(a, sms, s))

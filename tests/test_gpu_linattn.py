@@ -120,6 +120,8 @@ CASES = {
     # few heads and many chunks: the sequence is split into segments
     "split": dict(B=1, L=1500, H=1, KV=1, dk=64, dv=64),
     "split_lens": dict(B=2, L=1700, H=2, KV=1, dk=32, dv=64, lens=[1430, 400]),
+    # more heads than SMs, not a multiple: sequences are cut between two CTAs
+    "cut": dict(B=1, L=900, H=149, KV=149, dk=16, dv=24),
     "no_start": dict(B=2, L=200, H=2, KV=2, dk=128, dv=128, start=False),
     "split_no_start": dict(B=1, L=1500, H=1, KV=1, dk=128, dv=128, start=False),
 }
@@ -195,7 +197,7 @@ def test_a_prompt_then_tokens_is_the_longer_prompt(S, dtype):
     c.close(Case.f64(whole), r.out, r.once, r.mag, "o")
 
 
-@pytest.mark.parametrize("name", ["lens", "split", "split_lens", "shared"])
+@pytest.mark.parametrize("name", ["lens", "split", "split_lens", "shared", "cut"])
 def test_in_place_state_repeats_graphs_and_streams(S, name):
     """S_final over S0, two runs, a captured and replayed call, and a call on another stream give the same
     bits (every sum has a fixed order)."""
@@ -232,6 +234,23 @@ def test_in_place_state_repeats_graphs_and_streams(S, name):
     first = c.backward(S)
     again = c.backward(S)
     assert all(torch.equal(x, y) for x, y in zip(first, again))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_sequences_cut_between_ctas_are_whole(S, d):
+    """160 heads share the SMs chunk by chunk, 80 do not: the same bits, for outputs and gradients."""
+    c = Case(8, 1, 1900, 160, 160, d, d, "bf16", scale=0.1)
+    o, S_final = c.forward(S)
+    grads = c.backward(S)
+    for h in (0, 80):
+        part = Case(8, 1, 1900, 80, 80, d, d, "bf16", scale=0.1)
+        cut = lambda x: x[:, :, h:h + 80].contiguous()
+        part.q, part.k, part.v, part.g_o = (cut(x) for x in (c.q, c.k, c.v, c.g_o))
+        part.S0, part.g_S, part.g = c.S0[:, h:h + 80].contiguous(), c.g_S[:, h:h + 80].contiguous(), c.g[h:h + 80].contiguous()
+        po, pS = part.forward(S)
+        assert torch.equal(cut(o), po) and torch.equal(S_final[:, h:h + 80], pS)
+        for got, want in zip(grads[:3], part.backward(S)[:3]):
+            assert torch.equal(cut(got), want)
 
 
 def test_a_value_that_is_not_finite_stays_in_its_sequence(S):
