@@ -150,36 +150,53 @@ __global__ void __launch_bounds__(128) la_simt_kernel(const __grid_constant__ La
 
 // ---- segment chain -------------------------------------------------------------------------------------
 // seg[s] holds segment s's end state from zero; it becomes the state before segment s, and the state
-// after the last one goes to M_end. One thread per state element.
-__global__ void __launch_bounds__(256) la_chain_kernel(const __grid_constant__ LaParams p) {
-  const int64_t item = blockIdx.x, bhs = (int64_t)p.B * p.H;
+// after the last one goes to M_end. One thread per 4 elements of a row, their segments' states loaded
+// kBatch at a time (the stores in between would keep the compiler from moving the loads up).
+__global__ void __launch_bounds__(128) la_chain_kernel(const __grid_constant__ LaParams p) {
+  constexpr int kBatch = 8;
+  const uint32_t bhs = (uint32_t)p.B * p.H, item = blockIdx.x;
   const LaRole& r = p.role[item / bhs];
-  const int64_t bh = item % bhs;
-  const int b = (int)(bh / p.H), h = (int)(bh % p.H), size = r.dx * r.dw;
-  const int e = blockIdx.y * 256 + threadIdx.x;
+  const uint32_t bh = item % bhs;
+  const int b = (int)(bh / p.H), h = (int)(bh % p.H), dw = r.dw, size = r.dx * dw, rev = r.rev, nseg = p.nseg;
+  const int e = (blockIdx.y * 128 + threadIdx.x) * 4;
   if (e >= size) return;
-  const int j = e / r.dw, c = e - j * r.dw;
-  const float lg = p.g[h] * kLog2e;
+  const int j = e / dw, c = e - j * dw, sj = r.sj, sc = r.sc;
+  const float lg = p.g[h] * kLog2e, g_all = la_pow(lg, p.cps * kLaChunk);
   const int64_t len = la_len(p, b);
-  float* seg = r.seg + bh * p.nseg * size + e;
-  const int64_t own = bh * size + (int64_t)j * r.sj + (int64_t)c * r.sc;
-  float m = r.M0 ? r.M0[own] : 0.f;
-  constexpr int kBatch = 8;  // loads in flight: the stores in between keep the compiler from moving them up
-  for (int s0 = 0; s0 < p.nseg; s0 += kBatch) {
-    float end[kBatch];
+  float4* seg = reinterpret_cast<float4*>(r.seg + (int64_t)bh * nseg * size + e);
+  const int64_t own = (int64_t)bh * size + (int64_t)j * sj + (int64_t)c * sc;
+  const float* M0 = r.M0;
+  float* M_end = r.M_end;
+  float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (M0) m = make_float4(M0[own], M0[own + sc], M0[own + 2 * sc], M0[own + 3 * sc]);
+  for (int s0 = 0; s0 < nseg; s0 += kBatch) {
+    float4 end[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) end[i] = s0 + i < p.nseg ? seg[(int64_t)(s0 + i) * size] : 0.f;
+    for (int i = 0; i < kBatch; ++i)
+      if (s0 + i < nseg) end[i] = seg[(int64_t)(s0 + i) * (size / 4)];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      if (s0 + i >= p.nseg) break;
-      int c0, c1;
-      la_segment(p, len, s0 + i, r.rev, c0, c1);
-      const int64_t n = max((int64_t)0, min((int64_t)c1 * kLaChunk, len) - (int64_t)c0 * kLaChunk);
-      seg[(int64_t)(s0 + i) * size] = m;
-      if (n > 0) m = fmaf(la_pow(lg, (int)n), m, end[i]);
+      if (s0 + i < nseg) {
+        int c0, c1;
+        la_segment(p, len, s0 + i, rev, c0, c1);
+        const int n = (int)(min((int64_t)c1 * kLaChunk, len) - min((int64_t)c0 * kLaChunk, len));
+        seg[(int64_t)(s0 + i) * (size / 4)] = m;
+        if (n > 0) {
+          const float g = n == p.cps * kLaChunk ? g_all : la_pow(lg, n);
+          m.x = fmaf(g, m.x, end[i].x);
+          m.y = fmaf(g, m.y, end[i].y);
+          m.z = fmaf(g, m.z, end[i].z);
+          m.w = fmaf(g, m.w, end[i].w);
+        }
+      }
     }
   }
-  if (r.M_end) r.M_end[own] = m;
+  if (M_end) {
+    M_end[own] = m.x;
+    M_end[own + sc] = m.y;
+    M_end[own + 2 * sc] = m.z;
+    M_end[own + 3 * sc] = m.w;
+  }
 }
 
 // ---- rows without a token, shared heads ----------------------------------------------------------------
@@ -284,7 +301,8 @@ swimba_status check_la(const swimba_linattn_dims* d) {
 // Segments per sequence. Splitting a sequence costs a second pass over y and w (the segments' end
 // states), so it pays only where the heads alone leave SMs idle. The rule takes the split with the
 // least time in units of one chunk's outputs on one CTA: rounds of CTAs x chunks per segment, with
-// half a unit more per chunk for the state pass of a split sequence and two units per launch.
+// half a unit more per chunk for the state pass of a split sequence, two per segment for its state's way
+// through memory and four for the two launches more.
 LaPlan la_plan(const swimba_linattn_dims* d, int roles, bool tc) {
   const int64_t nch = (d->seqlen + kLaChunk - 1) / kLaChunk, heads = d->batch * d->n_heads * roles;
   const int64_t slots = tc ? kSMs : 4 * kSMs;
@@ -292,7 +310,7 @@ LaPlan la_plan(const swimba_linattn_dims* d, int roles, bool tc) {
   double least = (double)((heads + slots - 1) / slots) * nch;
   for (int64_t n = 2; n <= std::min<int64_t>(nch, 64); ++n) {
     const int64_t cps = (nch + n - 1) / n, segs = (nch + cps - 1) / cps;
-    const double t = (double)((heads * segs + slots - 1) / slots) * cps * 1.5 + 4;
+    const double t = (double)((heads * segs + slots - 1) / slots) * (cps * 1.5 + 2) + 4;
     if (t < least) {
       least = t;
       best = LaPlan{tc, (int)segs, (int)cps, false};
@@ -330,8 +348,8 @@ LaLayout la_layout(const swimba_linattn_dims* d, const LaPlan& pl, int roles) {
 }
 
 void launch_chain(const LaParams& p, cudaStream_t s) {
-  const dim3 grid((unsigned)((int64_t)p.n_roles * p.B * p.H), 64);  // 64 x 256 threads: up to 128 x 128 elements
-  la_chain_kernel<<<grid, 256, 0, s>>>(p);
+  const dim3 grid((unsigned)((int64_t)p.n_roles * p.B * p.H), 32);  // 32 x 128 threads: up to 128 x 128 elements
+  la_chain_kernel<<<grid, 128, 0, s>>>(p);
   note_launch();
 }
 

@@ -54,9 +54,8 @@ namespace {
 
 constexpr int kTile = kLaChunk * 128;  // 128 tokens x 128 bytes (64 bf16), 128-byte swizzle: 16 KB
 constexpr int kThreads = 768;
-// γ w ring: slots of 16 tokens (one MMA step) x 3 parts x 8 columns. Slots of 16 tokens rather than 32
-// let the warps that fill it refill a slot in half the time that its MMAs and theirs keep it busy.
-constexpr int kPart = 8, kStep = 16, kSteps = kLaChunk / kStep;
+// γ w ring: per 16 tokens (one MMA step) 3 parts x 8 columns.
+constexpr int kPart = 8, kStep = 16;
 constexpr uint32_t kColP = 0, kColO = 128;
 
 // An item's powers of γ by distance, with 32 zeros on the side that the mask hides: 0 .. 0 γ^0 .. γ^127, or
@@ -79,7 +78,10 @@ struct LaSmem {
   static constexpr int XB = DX / 64, WB = DW / 64;
   // Without scores and outputs there is room for two U and a longer ring, and the warps that would make
   // them fill it too.
-  static constexpr int NU = MODE == 0 ? 1 : 2, RING = MODE == 0 ? 4 : 8, SETS = MODE == 0 ? 2 : 4;
+  // A slot of the ring is one MMA step where columns are short, so that it is refilled in half the time, and
+  // two where there are enough: an issuing warp spends about 300 cycles on a slot, three MMAs take 192.
+  static constexpr int NU = MODE == 0 ? 1 : 2, RING = 4, SETS = MODE == 0 ? 2 : 4, SUB = MODE == 0 ? 1 : 2;
+  static constexpr int SLOTS = kLaChunk / (kStep * SUB);  // per chunk
   static constexpr uint32_t COL_U = MODE == 0 ? 256 : 0, COL_RING = MODE == 0 ? 384 : 256;
   static constexpr int TX = MODE == 0 ? XB * kTile : 0, TY = XB * kTile, TW = WB * kTile;  // one tile of each
   static constexpr int COPY = MODE == 0 ? DX * DW * 2 : 0;  // M's bf16 copy, [dw rows][dx], K-major
@@ -389,21 +391,24 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             // A poll queues up behind the MMAs issued before it; asked for after them, it left the tensor cores
             // about 140 cycles without work at every step. So each step's is issued before the MMAs of the
             // step before, and its answer is looked at after them.
-            constexpr int R = SM::RING;
-            bool here = mbar_try_wait(&ring_full[0], (it * (kSteps / R)) & 1);
+            constexpr int R = SM::RING, PER = SM::SLOTS / R;
+            bool here = mbar_try_wait(&ring_full[0], (it * PER) & 1);
 #pragma unroll 1
-            for (int k = 0; k < kSteps; ++k) {
-              if (!__all_sync(0xffffffffu, here) && !(ok = wait(&ring_full[k % R], (it * (kSteps / R) + k / R) & 1))) break;
+            for (int k = 0; k < SM::SLOTS; ++k) {
+              if (!__all_sync(0xffffffffu, here) && !(ok = wait(&ring_full[k % R], (it * PER + k / R) & 1))) break;
               tc_fence_after();
-              here = k + 1 < kSteps && mbar_try_wait(&ring_full[(k + 1) % R], (it * (kSteps / R) + (k + 1) / R) & 1);
+              here = k + 1 < SM::SLOTS && mbar_try_wait(&ring_full[(k + 1) % R], (it * PER + (k + 1) / R) & 1);
               if (elect_one()) {
 #pragma unroll
-                for (int part = 0; part < 3; ++part)
-                  if (part < 2 || t.parts == 3)
-                    mma_bf16_ts(tmem + SM::COL_U + ub * 128, tmem + SM::COL_RING + (k % R) * 3 * kPart + part * kPart,
-                                dMN + sY + k * (kStep * 8), id_u, (k | part) != 0);
+                for (int sub = 0; sub < SM::SUB; ++sub)
+#pragma unroll
+                  for (int part = 0; part < 3; ++part)
+                    if (part < 2 || t.parts == 3)
+                      mma_bf16_ts(tmem + SM::COL_U + ub * 128,
+                                  tmem + SM::COL_RING + ((k % R) * SM::SUB + sub) * 3 * kPart + part * kPart,
+                                  dMN + sY + (k * SM::SUB + sub) * (kStep * 8), id_u, (k | sub | part) != 0);
                 mma_commit(&ring_empty[k % R]);
-                if (k == kSteps - 1) mma_commit(&u_full[ub]);
+                if (k == SM::SLOTS - 1) mma_commit(&u_full[ub]);
               }
               __syncwarp();
             }
@@ -702,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     if (!active) {  // those rows stay zero
       const uint32_t z[8] = {};
 #pragma unroll 1
-      for (int k = 0; k < SM::RING * 3; ++k) tmem_st8(tl + SM::COL_RING + k * kPart, z);
+      for (int k = 0; k < SM::RING * SM::SUB * 3; ++k) tmem_st8(tl + SM::COL_RING + k * kPart, z);
       tmem_wait_st();
     }
     uint32_t it = 0, ii = 0;
@@ -721,44 +726,48 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         // holds channel t / 4 of tokens 2 (t % 4) + 0..1, scaled, split and stored in that form
         const uint32_t tw = smem_u32(sm) + SM::W + st * SM::TW + (wq >> 1) * kTile + ((lane & 7) + 8 * (lane >> 4)) * 128;
 #pragma unroll 1
-        for (int k = set; k < kSteps; k += SM::SETS) {
-          constexpr int R = SM::RING;
+        for (int k = set; k < SM::SLOTS; k += SM::SETS) {
+          constexpr int R = SM::RING, PER = SM::SLOTS / R;
           const uint32_t slot = k % R;
-          if (!(ok = wait(&ring_empty[slot], ((it * (kSteps / R) + k / R) & 1) ^ 1))) break;
+          if (!(ok = wait(&ring_empty[slot], ((it * PER + k / R) & 1) ^ 1))) break;
           tc_fence_after();
           if (active) {
-            uint32_t raw[2][4];
+#pragma unroll 1
+            for (int sub = 0; sub < SM::SUB; ++sub) {
+              const int step = k * SM::SUB + sub;
+              uint32_t raw[2][4];
 #pragma unroll
-            for (int half = 0; half < 2; ++half)  // 16 channels: matrices (tokens, channels) (0, 0), (0, 8), (8, 0), (8, 8)
-              ldmatrix_x4_trans(tw + k * (kStep * 128) + ((((wq & 1) * 4 + half * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4),
-                                raw[half]);
-            float2 wt[2];
-            uint32_t keep[2];
+              for (int half = 0; half < 2; ++half)  // 16 channels: matrices (tokens, channels) (0, 0), (0, 8), (8, 0), (8, 8)
+                ldmatrix_x4_trans(tw + step * (kStep * 128) + ((((wq & 1) * 4 + half * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4),
+                                  raw[half]);
+              float2 wt[2];
+              uint32_t keep[2];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              // γ^(n-1-s), reverse γ γ^s; tokens behind the last chunk's end count as zeros whatever they hold
-              const int s = kStep * k + 8 * g + 2 * (lane & 3), e = rev ? s : max(n - 2 - s, -1);
-              const float a0 = lds1(table + (rev ? -e : e + 1) * 4), a1 = lds1(table + (rev ? -e - 1 : e) * 4);
-              wt[g] = make_float2(a0 * f_w, a1 * f_w);
-              keep[g] = (s < n ? 0xffffu : 0u) | (s + 1 < n ? 0xffff0000u : 0u);
-            }
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t hi[4], mid[4], lo[4];
-#pragma unroll
-              for (int d = 0; d < 4; ++d) {
-                // three truncated parts of 8 bits each: their sum is the product's 24 bits
-                const uint32_t v = raw[half][d] & keep[d >> 1];
-                const float v0 = bf16lo(v) * wt[d >> 1].x, v1 = bf16hi(v) * wt[d >> 1].y;
-                hi[d] = high_halves(v0, v1);
-                const float r0 = v0 - top_bits(v0), r1 = v1 - top_bits(v1);
-                mid[d] = high_halves(r0, r1);
-                lo[d] = high_halves(r0 - top_bits(r0), r1 - top_bits(r1));
+              for (int g = 0; g < 2; ++g) {
+                // γ^(n-1-s), reverse γ γ^s; tokens behind the last chunk's end count as zeros whatever they hold
+                const int s = kStep * step + 8 * g + 2 * (lane & 3), e = rev ? s : max(n - 2 - s, -1);
+                const float a0 = lds1(table + (rev ? -e : e + 1) * 4), a1 = lds1(table + (rev ? -e - 1 : e) * 4);
+                wt[g] = make_float2(a0 * f_w, a1 * f_w);
+                keep[g] = (s < n ? 0xffffu : 0u) | (s + 1 < n ? 0xffff0000u : 0u);
               }
-              const uint32_t at = tl + ((uint32_t)(16 * half) << 16) + SM::COL_RING + slot * 3 * kPart;
-              tmem_st_16x128b_x2(at, hi);
-              tmem_st_16x128b_x2(at + kPart, mid);
-              if (t.parts == 3) tmem_st_16x128b_x2(at + 2 * kPart, lo);
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                  // three truncated parts of 8 bits each: their sum is the product's 24 bits
+                  const uint32_t v = raw[half][d] & keep[d >> 1];
+                  const float v0 = bf16lo(v) * wt[d >> 1].x, v1 = bf16hi(v) * wt[d >> 1].y;
+                  hi[d] = high_halves(v0, v1);
+                  const float r0 = v0 - top_bits(v0), r1 = v1 - top_bits(v1);
+                  mid[d] = high_halves(r0, r1);
+                  lo[d] = high_halves(r0 - top_bits(r0), r1 - top_bits(r1));
+                }
+                const uint32_t at = tl + ((uint32_t)(16 * half) << 16) + SM::COL_RING + (slot * SM::SUB + sub) * 3 * kPart;
+                tmem_st_16x128b_x2(at, hi);
+                tmem_st_16x128b_x2(at + kPart, mid);
+                if (t.parts == 3) tmem_st_16x128b_x2(at + 2 * kPart, lo);
+              }
             }
             tmem_wait_st();
           }
