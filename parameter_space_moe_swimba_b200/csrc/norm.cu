@@ -17,7 +17,9 @@
 // on their way: each thread copies the vectors of 8 channels that it will work on into shared memory of
 // its own (cp.async, no barrier), two rows ahead, and keeps its channels' weights and their gradients in
 // registers. Without the copies a row's loads waited for the row before it (16384 rows of 4096, bf16
-// with an fp32 residual, backward: 547 us, 2.7 TB/s). All sums are fp32 and taken in a fixed order.
+// with an fp32 residual, backward: 547 us, 2.7 TB/s); with 8 channels per thread a third of the
+// instructions were the row's sums and addresses, so a thread takes 16 where a row has more than 2048.
+// All sums are fp32 and taken in a fixed order.
 #include <algorithm>
 #include <type_traits>
 
@@ -69,7 +71,63 @@ __device__ __forceinline__ void store8(void* base, int64_t at, const float (&v)[
   }
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// 1 / (1 + e^-z) with the exp2 and reciprocal instructions (each within 2^-22).
+__device__ __forceinline__ float sigmoid(float z) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(-kLog2e * z)));
+  return r;
+}
+
+// Two floats in one 64-bit register pair: the packed fp32 instructions round each as the scalar ones do and
+// take half the issue slots, which bound the backward.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ float2 f2_split(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_sigmoid(F2 z) {
+  const float2 t = f2_split(z * f2(-kLog2e));
+  const float2 d = f2_split(f2(ex2_approx(t.x), ex2_approx(t.y)) + f2(1.f));
+  float a, b;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(d.y));
+  return f2(a, b);
+}
+template <typename T>
+__device__ __forceinline__ void store8(void* base, int64_t at, const F2 (&v)[4]) {
+  T* p = reinterpret_cast<T*>(base) + at;
+  const float2 a = f2_split(v[0]), b = f2_split(v[1]), c = f2_split(v[2]), d = f2_split(v[3]);
+  if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2(a.x, a.y), bf16x2(b.x, b.y), bf16x2(c.x, c.y), bf16x2(d.x, d.y));
+  } else {
+    reinterpret_cast<float4*>(p)[0] = make_float4(a.x, a.y, b.x, b.y);
+    reinterpret_cast<float4*>(p)[1] = make_float4(c.x, c.y, d.x, d.y);
+  }
+}
 
 // A row's threads: one warp of a CTA of four (WARP), or a whole CTA.
 template <bool WARP>
@@ -95,9 +153,11 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* red) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float s = lane < warps ? red[k * 16 + lane] : 0.f;
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      s += __shfl_xor_sync(0xffffffffu, s, 4);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
       v[k] = __shfl_sync(0xffffffffu, s, 0);
+      if (warps > 8) v[k] += __shfl_sync(0xffffffffu, s, 8);
     }
   }
 }
@@ -143,7 +203,7 @@ __device__ __forceinline__ void group_sum(float (&v)[NV], int nvec, int groups, 
     if (tid + i * tpr < nvec) v[i] = gsum[(tid + i * tpr) / gv];
 }
 
-constexpr int kRed = 64;     // floats of row_sum's shared memory: 16 + 32 + 16
+constexpr int kRed = 64;     // floats of row_sum's shared memory: 16 + 32 + 16; two sets, for even and odd rows
 constexpr int kInputs = 5;   // y, z, res, g_h, g_n
 
 // The row inputs: read from the thread's own copies in shared memory, which hold STAGES rows (one at work,
@@ -170,14 +230,15 @@ struct RowInputs {
     stage = 0;
     bytes = off;
   }
-  // Starts this thread's copies of a row into a stage (an empty group behind the last row).
-  __device__ __forceinline__ void fetch(int64_t r, int64_t rows, uint32_t st) {
+  // Starts this thread's copies of row r into a stage (an empty group behind the last row). `ahead` is the
+  // row's distance in channels from the tensors' beginnings.
+  __device__ __forceinline__ void fetch(int64_t r, int64_t rows, int64_t ahead, uint32_t st) {
     if constexpr (STAGES == 0) return;
     if (r < rows) {
 #pragma unroll
       for (int k = 0; k < kInputs; ++k) {
         if (!src[k]) continue;
-        const uint8_t* from = reinterpret_cast<const uint8_t*>(src[k]) + r * width * (kParts(k) * 2);
+        const uint8_t* from = reinterpret_cast<const uint8_t*>(src[k]) + ahead * (kParts(k) * 2);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int v = tid + i * tpr;
@@ -217,11 +278,24 @@ struct RowInputs {
       }
     }
   }
+  template <int K>
+  __device__ __forceinline__ void get(int i, F2 (&v)[4]) const {
+    float f[8];
+    get<K>(i, f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = f2(f[2 * e], f[2 * e + 1]);
+  }
 };
 
 // Shared memory of a row's threads: the cross-warp sums and, for groups that need it, group_sum's (both
 // rounded to 16 bytes), then the stages.
-__host__ __device__ inline int norm_sum_floats(int nvec, int groups) { return (kRed + nvec + groups + 3) & ~3; }
+__host__ __device__ inline bool norm_groups_in_smem(int nvec, int groups) {
+  const int gv = nvec / groups;
+  return groups > 1 && (gv > 32 || (gv & (gv - 1)) != 0);
+}
+__host__ __device__ inline int norm_sum_floats(int nvec, int groups) {
+  return (2 * kRed + (norm_groups_in_smem(nvec, groups) ? nvec + groups : 0) + 3) & ~3;
+}
 
 template <bool WARP>
 struct RowThreads {
@@ -232,18 +306,19 @@ struct RowThreads {
 };
 
 // ---- forward ---------------------------------------------------------------------------------------------
-template <typename IO, typename RES, int NV, bool WARP, int STAGES>
-__global__ void __launch_bounds__(WARP ? 128 : 512) norm_fwd_kernel(const NormParams p, int slot_bytes) {
+template <typename IO, typename RES, int NV, bool WARP, int STAGES, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) norm_fwd_kernel(const NormParams p, int slot_bytes) {
   extern __shared__ __align__(16) float smem[];
   const RowThreads<WARP> t;
   const int tid = t.tid, tpr = t.tpr, nvec = p.width / 8;
   float* red = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(smem) + t.slot * slot_bytes);
-  float* gred = red + kRed;
+  float* gred = red + 2 * kRed;
+  const bool group_smem = norm_groups_in_smem(nvec, p.groups);
   RowInputs<IO, RES, NV, STAGES> in(p, sm100::smem_u32(red + norm_sum_floats(nvec, p.groups)), tid, tpr);
   const int64_t first = (int64_t)blockIdx.x * t.per_cta + t.slot, step = (int64_t)gridDim.x * t.per_cta;
   const float inv = 1.f / (float)p.width, ginv = (float)p.groups / (float)p.width;
 #pragma unroll
-  for (int k = 0; k < STAGES - 1; ++k) in.fetch(first + k * step, p.rows, k);
+  for (int k = 0; k < STAGES - 1; ++k) in.fetch(first + k * step, p.rows, (first + k * step) * p.width, k);
   float wp[NV][8], wn[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -253,8 +328,11 @@ __global__ void __launch_bounds__(WARP ? 128 : 512) norm_fwd_kernel(const NormPa
     if (p.w_pre) load8<float>(p.w_pre, 8 * v, wn[i]);
   }
   uint32_t st = 0;
+  int red_row = 0;
+  int64_t ahead = (first + (STAGES - 1) * step) * p.width;
   for (int64_t row = first; row < p.rows; row += step) {
-    in.fetch(row + (STAGES - 1) * step, p.rows, st == 0 ? STAGES - 1 : st - 1);
+    in.fetch(row + (STAGES - 1) * step, p.rows, ahead, st == 0 ? STAGES - 1 : st - 1);
+    ahead += step * p.width;
     in.use(row, st);
     if (++st == STAGES) st = 0;
     float a[NV][8];
@@ -276,13 +354,18 @@ __global__ void __launch_bounds__(WARP ? 128 : 512) norm_fwd_kernel(const NormPa
       for (int e = 0; e < 8; ++e) s[i] = fmaf(a[i][e], a[i][e], s[i]);
     }
     if (p.w_post) {
-      group_sum<WARP, NV>(s, nvec, p.groups, tid, tpr, red, gred);
+      group_sum<WARP, NV>(s, nvec, p.groups, tid, tpr, red + red_row, gred);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const float r = rsqrtf(fmaf(s[i], ginv, p.eps));
+        const float r = rsqrtf(fmaf(s[i], ginv, p.eps)) * p.beta;
 #pragma unroll
         for (int e = 0; e < 8; ++e) a[i][e] *= r * wp[i][e];
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[i][e] *= p.beta;
     }
     float ss[1] = {0.f};
 #pragma unroll
@@ -299,13 +382,13 @@ __global__ void __launch_bounds__(WARP ? 128 : 512) norm_fwd_kernel(const NormPa
       if (p.res) in.template get<2>(i, r);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        a[i][e] = p.res ? fmaf(p.alpha, r[e], p.beta * a[i][e]) : p.beta * a[i][e];
+        if (p.res) a[i][e] = fmaf(p.alpha, r[e], a[i][e]);
         ss[0] = fmaf(a[i][e], a[i][e], ss[0]);
       }
       if (p.h) store8<RES>(p.h, row * p.width + 8 * v, a[i]);
     }
     if (p.n) {
-      row_sum<WARP, 1>(ss, red + 16);
+      row_sum<WARP, 1>(ss, red + red_row + 16);
       const float r = rsqrtf(fmaf(ss[0], inv, p.eps));
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -316,65 +399,79 @@ __global__ void __launch_bounds__(WARP ? 128 : 512) norm_fwd_kernel(const NormPa
         store8<IO>(p.n, row * p.width + 8 * v, a[i]);
       }
     }
-    row_sync<WARP>();  // the shared sums are free for the next row
+    // the next row's sums go into the other set; group_sum's shared memory has one
+    red_row ^= kRed;
+    if (group_smem) row_sync<WARP>();
   }
 }
 
 // ---- backward --------------------------------------------------------------------------------------------
 // A CTA writes its sums of the two weight gradients once, to be summed over the CTAs by norm_dw_kernel.
-template <typename IO, typename RES, int NV, bool WARP, int STAGES>
-__global__ void __launch_bounds__(WARP ? 128 : 512) norm_bwd_kernel(const NormParams p, int slot_bytes) {
+template <typename IO, typename RES, int NV, bool WARP, int STAGES, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(const NormParams p, int slot_bytes) {
   extern __shared__ __align__(16) float smem[];
   const RowThreads<WARP> t;
   const int tid = t.tid, tpr = t.tpr, nvec = p.width / 8;
   float* red = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(smem) + t.slot * slot_bytes);
-  float* gred = red + kRed;
+  float* gred = red + 2 * kRed;
+  const bool group_smem = norm_groups_in_smem(nvec, p.groups);
   RowInputs<IO, RES, NV, STAGES> in(p, sm100::smem_u32(red + norm_sum_floats(nvec, p.groups)), tid, tpr);
   const int64_t first = (int64_t)blockIdx.x * t.per_cta + t.slot, step = (int64_t)gridDim.x * t.per_cta;
   const float inv = 1.f / (float)p.width, ginv = (float)p.groups / (float)p.width;
 #pragma unroll
-  for (int k = 0; k < STAGES - 1; ++k) in.fetch(first + k * step, p.rows, k);
-  float wp[NV][8], wn[NV][8], dwp[NV][8], dwn[NV][8];
+  for (int k = 0; k < STAGES - 1; ++k) in.fetch(first + k * step, p.rows, (first + k * step) * p.width, k);
+  F2 wp[NV][4], wn[NV][4], dwp[NV][4], dwn[NV][4];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = tid + i * tpr;
+    float a[8] = {}, b[8] = {};
+    if (v < nvec && p.w_post) load8<float>(p.w_post, 8 * v, a);
+    if (v < nvec && p.w_pre) load8<float>(p.w_pre, 8 * v, b);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) wp[i][e] = wn[i][e] = dwp[i][e] = dwn[i][e] = 0.f;
-    if (v >= nvec) continue;
-    if (p.w_post) load8<float>(p.w_post, 8 * v, wp[i]);
-    if (p.w_pre) load8<float>(p.w_pre, 8 * v, wn[i]);
+    for (int e = 0; e < 4; ++e) {
+      wp[i][e] = p.w_post ? f2(a[2 * e], a[2 * e + 1]) : f2(1.f);
+      wn[i][e] = f2(b[2 * e], b[2 * e + 1]);
+      dwp[i][e] = dwn[i][e] = f2(0.f);
+    }
   }
+  const bool gate_first = p.z && !p.gate_last, gate_last = p.z && p.gate_last;
   uint32_t st = 0;
+  int red_row = 0;
+  int64_t ahead = (first + (STAGES - 1) * step) * p.width;
   for (int64_t row = first; row < p.rows; row += step) {
-    in.fetch(row + (STAGES - 1) * step, p.rows, st == 0 ? STAGES - 1 : st - 1);
+    in.fetch(row + (STAGES - 1) * step, p.rows, ahead, st == 0 ? STAGES - 1 : st - 1);
+    ahead += step * p.width;
     in.use(row, st);
     if (++st == STAGES) st = 0;
     const int64_t base = row * p.width;
     // the forward: a, its norm, h
-    float hat[NV][8], h[NV][8], r[NV];
+    F2 hat[NV][4], h[NV][4];
+    float r[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       r[i] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) hat[i][e] = h[i][e] = 0.f;
+      for (int e = 0; e < 4; ++e) hat[i][e] = h[i][e] = f2(0.f);
       if (tid + i * tpr >= nvec) continue;
       if (p.y) in.template get<0>(i, hat[i]);
-      if (p.z && !p.gate_last) {
-        float z[8];
+      if (gate_first) {
+        F2 z[4];
         in.template get<1>(i, z);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) hat[i][e] *= z[e] * sigmoid(z[e]);
+        for (int e = 0; e < 4; ++e) hat[i][e] = hat[i][e] * (z[e] * f2_sigmoid(z[e]));
       }
+      F2 q = f2(0.f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) r[i] = fmaf(hat[i][e], hat[i][e], r[i]);
+      for (int e = 0; e < 4; ++e) q = f2_fma(hat[i][e], hat[i][e], q);
+      r[i] = f2_split(q).x + f2_split(q).y;
     }
     if (p.w_post) {
-      group_sum<WARP, NV>(r, nvec, p.groups, tid, tpr, red, gred);
+      group_sum<WARP, NV>(r, nvec, p.groups, tid, tpr, red + red_row, gred);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         r[i] = rsqrtf(fmaf(r[i], ginv, p.eps));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) hat[i][e] *= r[i];
+        for (int e = 0; e < 4; ++e) hat[i][e] = hat[i][e] * f2(r[i]);
       }
     }
     float s[2] = {0.f, 0.f};
@@ -382,20 +479,23 @@ __global__ void __launch_bounds__(WARP ? 128 : 512) norm_bwd_kernel(const NormPa
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (tid + i * tpr >= nvec) continue;
-        float z[8], gn[8];
-        if (p.z && p.gate_last) in.template get<1>(i, z);
+        F2 z[4], gn[4];
+        if (gate_last) in.template get<1>(i, z);
         if (p.res) in.template get<2>(i, h[i]);
         in.template get<4>(i, gn);
+        F2 s0 = f2(0.f), s1 = f2(0.f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float q = p.w_post ? hat[i][e] * wp[i][e] : hat[i][e];
-          if (p.z && p.gate_last) q *= z[e] * sigmoid(z[e]);
-          h[i][e] = fmaf(p.alpha, h[i][e], p.beta * q);
-          s[0] = fmaf(h[i][e], h[i][e], s[0]);
-          s[1] = fmaf(gn[e] * wn[i][e], h[i][e], s[1]);
+        for (int e = 0; e < 4; ++e) {
+          F2 q = hat[i][e] * (wp[i][e] * f2(p.beta));
+          if (gate_last) q = q * (z[e] * f2_sigmoid(z[e]));
+          h[i][e] = f2_fma(f2(p.alpha), h[i][e], q);
+          s0 = f2_fma(h[i][e], h[i][e], s0);
+          s1 = f2_fma(gn[e] * wn[i][e], h[i][e], s1);
         }
+        s[0] += f2_split(s0).x + f2_split(s0).y;
+        s[1] += f2_split(s1).x + f2_split(s1).y;
       }
-      row_sum<WARP, 2>(s, red + 16);
+      row_sum<WARP, 2>(s, red + red_row + 16);
     }
     const float rh = p.g_n ? rsqrtf(fmaf(s[0], inv, p.eps)) : 0.f, m = s[1] * rh * inv;
     // back through the norm before the next block, the residual, the gate behind the norm
@@ -405,75 +505,76 @@ __global__ void __launch_bounds__(WARP ? 128 : 512) norm_bwd_kernel(const NormPa
       const int v = tid + i * tpr;
       q[i] = 0.f;
       if (v >= nvec) continue;
-      float dh[8] = {};
+      F2 dh[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
       if (p.g_h) in.template get<3>(i, dh);
       if (p.g_n) {
-        float gn[8];
+        F2 gn[4];
         in.template get<4>(i, gn);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float hh = h[i][e] * rh;
-          dwn[i][e] = fmaf(gn[e], hh, dwn[i][e]);
-          dh[e] = fmaf(rh, fmaf(-hh, m, gn[e] * wn[i][e]), dh[e]);
+        for (int e = 0; e < 4; ++e) {
+          const F2 hh = h[i][e] * f2(rh);
+          dwn[i][e] = f2_fma(gn[e], hh, dwn[i][e]);
+          dh[e] = f2_fma(f2(rh), f2_fma(hh, f2(-m), gn[e] * wn[i][e]), dh[e]);
         }
       }
       if (p.dres) {
-        float d[8];
+        F2 d[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] = p.alpha * dh[e];
+        for (int e = 0; e < 4; ++e) d[e] = dh[e] * f2(p.alpha);
         store8<RES>(p.dres, base + 8 * v, d);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) dh[e] *= p.beta;
-      if (p.z && p.gate_last) {
-        float z[8], dz[8];
+      for (int e = 0; e < 4; ++e) dh[e] = dh[e] * f2(p.beta);
+      if (gate_last) {
+        F2 z[4], dz[4];
         in.template get<1>(i, z);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float sg = sigmoid(z[e]);
-          dz[e] = dh[e] * (p.w_post ? hat[i][e] * wp[i][e] : hat[i][e]) * (sg * fmaf(z[e], 1.f - sg, 1.f));
-          dh[e] *= z[e] * sg;
+        for (int e = 0; e < 4; ++e) {
+          const F2 sg = f2_sigmoid(z[e]);
+          dz[e] = dh[e] * (hat[i][e] * wp[i][e]) * (sg * f2_fma(z[e], f2_fma(sg, f2(-1.f), f2(1.f)), f2(1.f)));
+          dh[e] = dh[e] * (z[e] * sg);
         }
         store8<IO>(p.dz, base + 8 * v, dz);
       }
+      F2 qq = f2(0.f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (p.w_post) {
-          dwp[i][e] = fmaf(dh[e], hat[i][e], dwp[i][e]);
-          dh[e] *= wp[i][e];
-          q[i] = fmaf(dh[e], hat[i][e], q[i]);
-        }
-        h[i][e] = dh[e];
+      for (int e = 0; e < 4; ++e) {
+        dwp[i][e] = f2_fma(dh[e], hat[i][e], dwp[i][e]);
+        h[i][e] = dh[e] * wp[i][e];
+        qq = f2_fma(h[i][e], hat[i][e], qq);
       }
+      q[i] = f2_split(qq).x + f2_split(qq).y;
     }
     // the norm after the mixer and the gate before it
-    if (p.w_post) group_sum<WARP, NV>(q, nvec, p.groups, tid, tpr, red + 48, gred);
+    if (p.w_post) group_sum<WARP, NV>(q, nvec, p.groups, tid, tpr, red + red_row + 48, gred);
     if (p.y) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = tid + i * tpr;
         if (v >= nvec) continue;
         if (p.w_post) {
-          const float mq = q[i] * ginv;
+          const float mq = -q[i] * ginv;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) h[i][e] = r[i] * fmaf(-hat[i][e], mq, h[i][e]);
+          for (int e = 0; e < 4; ++e) h[i][e] = f2(r[i]) * f2_fma(hat[i][e], f2(mq), h[i][e]);
         }
-        if (p.z && !p.gate_last) {
-          float y[8], z[8], dz[8];
+        if (gate_first) {
+          F2 y[4], z[4], dz[4];
           in.template get<0>(i, y);
           in.template get<1>(i, z);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float sg = sigmoid(z[e]);
-            dz[e] = h[i][e] * y[e] * (sg * fmaf(z[e], 1.f - sg, 1.f));
-            h[i][e] *= z[e] * sg;
+          for (int e = 0; e < 4; ++e) {
+            const F2 sg = f2_sigmoid(z[e]);
+            dz[e] = h[i][e] * y[e] * (sg * f2_fma(z[e], f2_fma(sg, f2(-1.f), f2(1.f)), f2(1.f)));
+            h[i][e] = h[i][e] * (z[e] * sg);
           }
           store8<IO>(p.dz, base + 8 * v, dz);
         }
         store8<IO>(p.dy, base + 8 * v, h[i]);
       }
     }
-    row_sync<WARP>();  // the shared sums are free for the next row
+    // the next row's sums go into the other set; group_sum's shared memory has one
+    red_row ^= kRed;
+    if (group_smem) row_sync<WARP>();
   }
   pdl_trigger();
   if (p.part == nullptr) return;
@@ -488,11 +589,12 @@ __global__ void __launch_bounds__(WARP ? 128 : 512) norm_bwd_kernel(const NormPa
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           float* d = part + (size_t)w * p.width + 8 * v;
-          const float(&a)[8] = w ? dwn[i] : dwp[i];
-          float o[8] = {};
-          if (k > 0) load8<float>(d, 0, o);
+          F2 o[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] += a[e];
+          for (int e = 0; e < 4; ++e) {
+            o[e] = w ? dwn[i][e] : dwp[i][e];
+            if (k > 0) o[e] = o[e] + f2(d[2 * e], d[2 * e + 1]);
+          }
           store8<float>(d, 0, o);
         }
       }
@@ -535,11 +637,8 @@ swimba_status check_norm(const swimba_norm_dims* d) {
   return SWIMBA_OK;
 }
 
-// Threads per row: one per vector of 8 channels, in whole warps, up to 512; two or four vectors each
-// above 4096 and 8192 channels.
-int threads_per_row(int width) { return std::min(512, (width / 8 + 31) / 32 * 32); }
-
-// How a call runs: threads per CTA, rows that a CTA works on at a time, CTAs, shared memory per row at work.
+// How a call runs: threads per CTA, rows that a CTA works on at a time, CTAs, shared memory per row at work,
+// vectors of 8 channels per thread, rows in shared memory.
 struct NormPlan {
   int threads, per_cta, ctas, slot_bytes, nv, stages;
   bool warp;
@@ -547,29 +646,38 @@ struct NormPlan {
 
 NormPlan norm_plan(const swimba_norm_dims* d, bool bwd) {
   NormPlan n{};
-  const int nvec = d->width / 8, tpr = threads_per_row(d->width);
-  n.warp = tpr == 32;
+  const int nvec = d->width / 8;
+  // one vector per thread up to 2048 channels, two up to 8192, four up to 16384, in whole warps
+  n.nv = nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4;
+  n.warp = nvec <= 32;
+  const int tpr = n.warp ? 32 : ((nvec + n.nv - 1) / n.nv + 31) / 32 * 32;
   n.threads = n.warp ? 128 : tpr;
   n.per_cta = n.warp ? 4 : 1;
-  n.nv = nvec <= tpr ? 1 : nvec <= 2 * tpr ? 2 : 4;
-  // as many stages as 200 KB hold (as if every input were given)
+  // as many rows in shared memory, up to three, as fit (as if every input were given) where a CTA has
+  // up to 256 threads beside another one (113 KB each), else alone (226 KB)
   const size_t io = d->io_dtype == SWIMBA_BF16 ? 2 : 4, res = d->res_dtype == SWIMBA_BF16 ? 2 : 4;
   const size_t sums = (size_t)norm_sum_floats(nvec, d->groups) * 4;
   const size_t stage = (size_t)n.nv * tpr * 8 * (bwd ? 3 * io + 2 * res : 2 * io + res);
-  const int most = n.nv == 1 ? 3 : 2;
-  n.stages = most;
-  while (n.stages > 0 && (sums + n.stages * stage) * n.per_cta > 200 * 1024) n.stages = n.stages == 3 ? 2 : 0;
+  const size_t pair = 113 * 1024, alone = 226 * 1024;
+  auto fits = [&](int st, size_t room) { return (sums + st * stage) * n.per_cta <= room; };
+  if (n.threads <= 256) n.stages = fits(3, pair) ? 3 : fits(2, pair) ? 2 : 1;
+  else n.stages = fits(2, alone) ? 2 : 0;
   n.slot_bytes = (int)(sums + n.stages * stage);
-  const int fit = (int)std::min<size_t>(200 * 1024 / ((size_t)n.slot_bytes * n.per_cta), 8);
-  const int per_sm = std::max(1, std::min(fit, (bwd ? 512 : 1024) / n.threads));
-  n.ctas = (int)std::min<int64_t>((d->rows + n.per_cta - 1) / n.per_cta, (int64_t)kSMs * per_sm);
+  const int fit = (int)std::min<size_t>(alone / ((size_t)n.slot_bytes * n.per_cta), 8);
+  // (the backward's registers allow 512 threads of two vectors, 768 of one); no more CTAs than share the
+  // rows evenly, since each writes its partial weight gradients
+  const int per_sm = std::max(1, std::min(fit, (bwd ? (n.nv == 1 ? 768 : 512) : 1024) / n.threads));
+  const int64_t units = (d->rows + n.per_cta - 1) / n.per_cta, rounds = (units + kSMs * per_sm - 1) / (kSMs * per_sm);
+  n.ctas = (int)((units + rounds - 1) / rounds);
   return n;
 }
 
-template <typename IO, typename RES, int NV, bool WARP, int STAGES>
+template <typename IO, typename RES, int NV, bool WARP, int STAGES, int MAXT>
 cudaError_t launch_norm(const NormPlan& n, const NormParams& p, bool bwd, cudaStream_t s) {
   const int smem = n.slot_bytes * n.per_cta;
-  auto kernel = bwd ? norm_bwd_kernel<IO, RES, NV, WARP, STAGES> : norm_fwd_kernel<IO, RES, NV, WARP, STAGES>;
+  if (n.stages != STAGES || n.nv != NV || n.threads > MAXT) return cudaErrorInvalidConfiguration;
+  auto kernel = bwd ? norm_bwd_kernel<IO, RES, NV, WARP, STAGES, MAXT>
+                    : norm_fwd_kernel<IO, RES, NV, WARP, STAGES, MAXT>;
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -582,12 +690,20 @@ cudaError_t launch_norm(const NormPlan& n, const NormParams& p, bool bwd, cudaSt
 template <typename IO, typename RES>
 cudaError_t run_norm(const swimba_norm_dims* d, const NormParams& p, bool bwd, cudaStream_t s) {
   const NormPlan n = norm_plan(d, bwd);
-  if (n.warp) return launch_norm<IO, RES, 1, true, 3>(n, p, bwd, s);
-  if (n.nv == 1)  // two stages of 4096 channels always fit
-    return n.stages == 3 ? launch_norm<IO, RES, 1, false, 3>(n, p, bwd, s) : launch_norm<IO, RES, 1, false, 2>(n, p, bwd, s);
+  // (up to 256 channels three rows always fit, up to 2048 two, up to 4096 one)
+  if (n.warp) return launch_norm<IO, RES, 1, true, 3, 128>(n, p, bwd, s);
+  if (n.nv == 1)
+    return n.stages == 3 ? launch_norm<IO, RES, 1, false, 3, 256>(n, p, bwd, s)
+                         : launch_norm<IO, RES, 1, false, 2, 256>(n, p, bwd, s);
+  if (n.nv == 2 && n.threads <= 256)
+    return n.stages == 3   ? launch_norm<IO, RES, 2, false, 3, 256>(n, p, bwd, s)
+           : n.stages == 2 ? launch_norm<IO, RES, 2, false, 2, 256>(n, p, bwd, s)
+                           : launch_norm<IO, RES, 2, false, 1, 256>(n, p, bwd, s);
   if (n.nv == 2)
-    return n.stages == 2 ? launch_norm<IO, RES, 2, false, 2>(n, p, bwd, s) : launch_norm<IO, RES, 2, false, 0>(n, p, bwd, s);
-  return n.stages == 2 ? launch_norm<IO, RES, 4, false, 2>(n, p, bwd, s) : launch_norm<IO, RES, 4, false, 0>(n, p, bwd, s);
+    return n.stages == 2 ? launch_norm<IO, RES, 2, false, 2, 512>(n, p, bwd, s)
+                         : launch_norm<IO, RES, 2, false, 0, 512>(n, p, bwd, s);
+  return n.stages == 2 ? launch_norm<IO, RES, 4, false, 2, 512>(n, p, bwd, s)
+                       : launch_norm<IO, RES, 4, false, 0, 512>(n, p, bwd, s);
 }
 
 cudaError_t run_norm_types(const swimba_norm_dims* d, const NormParams& p, bool bwd, cudaStream_t s) {
