@@ -48,11 +48,14 @@ __global__ void __launch_bounds__(128) la_simt_kernel(const __grid_constant__ La
   const int c_base = blockIdx.y * kSimtCols;
   if (c_base >= r.dw) return;
   const int ncol = min(kSimtCols, r.dw - c_base);
-  const float lg = p.g[h] * kLog2e, gamma = la_pow(lg, 1);
+  // γ's rounding would grow with every token that a state outlives: `slip`, its relative error, is taken out
+  // of the state after every kSimtTokens tokens (without it 4e-6 in place of 3e-7 at 333 tokens).
+  const double exact = exp((double)p.g[h]);
+  const float gamma = (float)exact, slip = gamma > 0.f ? (float)((exact - (double)gamma) / (double)gamma) : 0.f;
   const int64_t len = la_len(p, b);
   int c0, c1;
   la_segment(p, len, seg, r.rev, c0, c1);
-  const int64_t lo = (int64_t)c0 * kLaChunk, hi = min((int64_t)c1 * kLaChunk, len);
+  const int64_t lo = (int64_t)c0 * p.chunk, hi = min((int64_t)c1 * p.chunk, len);
 
   float M[NI * 4][2];
   const float* start = p.nseg > 1 ? r.seg + (bh * p.nseg + seg) * r.dx * r.dw : r.M0 ? r.M0 + bh * r.dx * r.dw : nullptr;
@@ -92,6 +95,12 @@ __global__ void __launch_bounds__(128) la_simt_kernel(const __grid_constant__ La
     stage(r.y, sy[0], NI * 16, 0, r.dx, r.dx, 1.f);
     stage(r.w, sw[0], kSimtCols, c_base, ncol, r.dw, r.s_u);
     __syncthreads();
+    const float slip_n = slip * (float)n;
+#pragma unroll
+    for (int i = 0; i < NI * 4; ++i) {
+      M[i][0] = fmaf(M[i][0], slip_n, M[i][0]);
+      M[i][1] = fmaf(M[i][1], slip_n, M[i][1]);
+    }
     for (int t = 0; t < n; ++t) {
       const float2 w = *reinterpret_cast<const float2*>(&sw[t][col]);
       float a0 = 0.f, a1 = 0.f;
@@ -161,7 +170,7 @@ __global__ void __launch_bounds__(128) la_chain_kernel(const __grid_constant__ L
   const int e = (blockIdx.y * 128 + threadIdx.x) * 4;
   if (e >= size) return;
   const int j = e / dw, c = e - j * dw, sj = r.sj, sc = r.sc;
-  const float lg = p.g[h] * kLog2e, g_all = la_pow(lg, p.cps * kLaChunk);
+  const float lg = p.g[h] * kLog2e, g_all = la_pow(lg, p.cps * p.chunk);
   const int64_t len = la_len(p, b);
   float4* seg = reinterpret_cast<float4*>(r.seg + (int64_t)bh * nseg * size + e);
   const int64_t own = (int64_t)bh * size + (int64_t)j * sj + (int64_t)c * sc;
@@ -179,10 +188,10 @@ __global__ void __launch_bounds__(128) la_chain_kernel(const __grid_constant__ L
       if (s0 + i < nseg) {
         int c0, c1;
         la_segment(p, len, s0 + i, rev, c0, c1);
-        const int n = (int)(min((int64_t)c1 * kLaChunk, len) - min((int64_t)c0 * kLaChunk, len));
+        const int n = (int)(min((int64_t)c1 * p.chunk, len) - min((int64_t)c0 * p.chunk, len));
         seg[(int64_t)(s0 + i) * (size / 4)] = m;
         if (n > 0) {
-          const float g = n == p.cps * kLaChunk ? g_all : la_pow(lg, n);
+          const float g = n == p.cps * p.chunk ? g_all : la_pow(lg, n);
           m.x = fmaf(g, m.x, end[i].x);
           m.y = fmaf(g, m.y, end[i].y);
           m.z = fmaf(g, m.z, end[i].z);
@@ -226,18 +235,21 @@ __global__ void __launch_bounds__(256) la_rows_kernel(IO* out, int64_t st, int64
 }
 
 // ---- decode step ----------------------------------------------------------------------------------------
-// One CTA per (sequence, head): the state is read and written once (8 d_k d_v bytes), which bounds it.
-// Threads go over the state row by row, 16 bytes each; the partial readouts of the threads that share
-// columns meet in shared memory.
+// One CTA per (sequence, head) and `cols` columns: the state is read and written once (8 d_k d_v bytes),
+// which bounds it: 1 GiB of state in 189 us, 88 % of the measured copy rate. Threads go over the state row
+// by row, 16 bytes each; the partial readouts of the threads that share columns meet in shared memory.
+// Few heads are cut into 32 columns (128 bytes of a row), so that every SM has a share.
 template <typename IO>
 __global__ void __launch_bounds__(256) la_step_kernel(LaStream q, LaStream k, LaStream v, const float* g,
                                                       const float* S_in, IO* o, float* S_out, int H, int dk, int dv,
-                                                      float scale) {
+                                                      int cols, float scale) {
   __shared__ float sq[128], sk[128];
   __shared__ __align__(16) float red[1024];
   const int64_t bh = blockIdx.x;
-  const int b = (int)(bh / H), h = (int)(bh % H), tid = threadIdx.x;
-  const int c4 = dv / 4, R = 256 / c4, r0 = tid / c4, c = tid - r0 * c4;
+  const int b = (int)(bh / H), h = (int)(bh % H), tid = threadIdx.x, first = blockIdx.y * cols;
+  const int mine = min(cols, dv - first), c4 = mine / 4, R = 256 / c4, r0 = tid / c4, c = tid - r0 * c4, pitch = dv / 4;
+  const float4* in = reinterpret_cast<const float4*>(S_in + bh * dk * dv + first) + c;
+  float4* out = reinterpret_cast<float4*>(S_out + bh * dk * dv + first) + c;
   if (tid < dk) {
     sq[tid] = to_f32(la_row<IO>(q, b, 0, h, dk)[tid]) * scale;
     sk[tid] = to_f32(la_row<IO>(k, b, 0, h, dk)[tid]);
@@ -245,32 +257,38 @@ __global__ void __launch_bounds__(256) la_step_kernel(LaStream q, LaStream k, La
   const float gamma = la_pow(g[h] * kLog2e, 1);
   __syncthreads();
   if (r0 < R) {
-    const IO* vp = la_row<IO>(v, b, 0, h, dv) + 4 * c;
+    const IO* vp = la_row<IO>(v, b, 0, h, dv) + first + 4 * c;
     const float4 vv = make_float4(to_f32(vp[0]), to_f32(vp[1]), to_f32(vp[2]), to_f32(vp[3]));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4* in = reinterpret_cast<const float4*>(S_in + bh * dk * dv);
-    float4* out = reinterpret_cast<float4*>(S_out + bh * dk * dv);
-#pragma unroll 8
-    for (int j = r0; j < dk; j += R) {
-      float4 s = in[(int64_t)j * c4 + c];
-      const float kj = sk[j], qj = sq[j];
-      s.x = fmaf(gamma, s.x, kj * vv.x);
-      s.y = fmaf(gamma, s.y, kj * vv.y);
-      s.z = fmaf(gamma, s.z, kj * vv.z);
-      s.w = fmaf(gamma, s.w, kj * vv.w);
-      acc.x = fmaf(qj, s.x, acc.x);
-      acc.y = fmaf(qj, s.y, acc.y);
-      acc.z = fmaf(qj, s.z, acc.z);
-      acc.w = fmaf(qj, s.w, acc.w);
-      out[(int64_t)j * c4 + c] = s;
+    constexpr int kBatch = 8;  // rows in flight
+    for (int j0 = r0; j0 < dk; j0 += kBatch * R) {
+      float4 s[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (j0 + i * R < dk) s[i] = in[(int64_t)(j0 + i * R) * pitch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int j = j0 + i * R;
+        if (j >= dk) break;
+        const float kj = sk[j], qj = sq[j];
+        s[i].x = fmaf(gamma, s[i].x, kj * vv.x);
+        s[i].y = fmaf(gamma, s[i].y, kj * vv.y);
+        s[i].z = fmaf(gamma, s[i].z, kj * vv.z);
+        s[i].w = fmaf(gamma, s[i].w, kj * vv.w);
+        acc.x = fmaf(qj, s[i].x, acc.x);
+        acc.y = fmaf(qj, s[i].y, acc.y);
+        acc.z = fmaf(qj, s[i].z, acc.z);
+        acc.w = fmaf(qj, s[i].w, acc.w);
+        out[(int64_t)j * pitch] = s[i];
+      }
     }
     reinterpret_cast<float4*>(red)[r0 * c4 + c] = acc;
   }
   __syncthreads();
-  if (tid < dv) {
+  if (tid < mine) {
     float a = 0.f;
-    for (int r = 0; r < R; ++r) a += red[r * dv + tid];
-    from_f32(o[bh * dv + tid], a);
+    for (int r = 0; r < R; ++r) a += red[r * mine + tid];
+    from_f32(o[bh * dv + first + tid], a);
   }
 }
 
@@ -301,16 +319,21 @@ swimba_status check_la(const swimba_linattn_dims* d) {
 // Segments per sequence. Splitting a sequence costs a second pass over y and w (the segments' end
 // states), so it pays only where the heads alone leave SMs idle. The rule takes the split with the
 // least time in units of one chunk's outputs on one CTA: rounds of CTAs x chunks per segment, with
-// half a unit more per chunk for the state pass of a split sequence, two per segment for its state's way
-// through memory and four for the two launches more.
+// `pass` units more per chunk for the state pass of a split sequence, `state` per segment for its
+// state's way through memory and `launch` for the two launches more. Tensor cores (a unit is about 3 us):
+// 16 heads x 65536 tokens take 0.36 ms in 9 segments, 2.1 ms whole. fp32 (32 tokens, 8 us): 48 roles x
+// 333 tokens take 76 us in segments, 176 us whole.
 LaPlan la_plan(const swimba_linattn_dims* d, int roles, bool tc) {
-  const int64_t nch = (d->seqlen + kLaChunk - 1) / kLaChunk, heads = d->batch * d->n_heads * roles;
+  const int chunk = tc ? kLaChunk : kLaSimtChunk;
+  const int64_t nch = (d->seqlen + chunk - 1) / chunk;
+  const int64_t heads = d->batch * d->n_heads * roles * (tc ? 1 : (std::max(d->d_k, d->d_v) + kSimtCols - 1) / kSimtCols);
   const int64_t slots = tc ? kSMs : 4 * kSMs;
+  const double pass = tc ? 0.5 : 0.7, state = tc ? 2 : 0.3, launch = tc ? 4 : 0.7;
   LaPlan best{tc, 1, (int)nch, tc};
   double least = (double)((heads + slots - 1) / slots) * nch;
   for (int64_t n = 2; n <= std::min<int64_t>(nch, 64); ++n) {
     const int64_t cps = (nch + n - 1) / n, segs = (nch + cps - 1) / cps;
-    const double t = (double)((heads * segs + slots - 1) / slots) * (cps * 1.5 + 2) + 4;
+    const double t = (double)((heads * segs + slots - 1) / slots) * (cps * (1 + pass) + state) + launch;
     if (t < least) {
       least = t;
       best = LaPlan{tc, (int)segs, (int)cps, false};
@@ -374,7 +397,7 @@ cudaError_t run_simt(const LaParams& p, cudaStream_t s) {
   }
   if (dx <= 32) return launch_simt<2>(p, dw, s);
   if (dx <= 64) return launch_simt<4>(p, dw, s);
-  return launch_simt<8>(p, dw, s);
+  return dx <= 96 ? launch_simt<6>(p, dw, s) : launch_simt<8>(p, dw, s);
 }
 
 // The tensor-core kernel takes roles of one padded size (64 or 128) together: all three where d_k and
@@ -425,6 +448,7 @@ LaParams la_params(const swimba_linattn_dims* d, const LaPlan& pl, const LaLayou
   p.L = d->seqlen;
   p.B = (int)d->batch;
   p.H = d->n_heads;
+  p.chunk = pl.tc ? kLaChunk : kLaSimtChunk;
   p.nseg = pl.nseg;
   p.cps = pl.cps;
   p.status = ws;
@@ -493,14 +517,16 @@ swimba_status swimba_linattn_step(const swimba_linattn_dims* dims, const void* q
   const int group = dims->n_heads / dims->n_kv_heads;
   const LaStream sq = la_stream(q, dims->q_stride, 1, 1), sk = la_stream(k, dims->k_stride, 1, group),
                  sv = la_stream(v, dims->v_stride, 1, group);
-  const unsigned grid = (unsigned)(dims->batch * dims->n_heads);
+  const int64_t heads = dims->batch * dims->n_heads;
+  const int cols = heads < 2 * kSMs ? 32 : 128;
+  const dim3 grid((unsigned)heads, (unsigned)((dims->d_v + cols - 1) / cols));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dims->io_dtype == SWIMBA_BF16)
     la_step_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(sq, sk, sv, log_decay, S_in, static_cast<__nv_bfloat16*>(o),
-                                                      S_out, dims->n_heads, dims->d_k, dims->d_v, dims->scale);
+                                                      S_out, dims->n_heads, dims->d_k, dims->d_v, cols, dims->scale);
   else
     la_step_kernel<float><<<grid, 256, 0, s>>>(sq, sk, sv, log_decay, S_in, static_cast<float*>(o), S_out,
-                                               dims->n_heads, dims->d_k, dims->d_v, dims->scale);
+                                               dims->n_heads, dims->d_k, dims->d_v, cols, dims->scale);
   note_launch();
   return api_cuda_status(cudaGetLastError());
 }

@@ -14,7 +14,8 @@
 
 namespace swimba {
 
-constexpr int kLaChunk = 128;   // tokens per chunk; segments are whole chunks
+constexpr int kLaChunk = 128;   // tokens per chunk of the tensor-core kernel
+constexpr int kLaSimtChunk = 32;  // the fp32 recurrence's segments are whole multiples of this
 constexpr int kLaMaxRoles = 3;
 
 // Element (b, t, h, j) of an io tensor: p + b sb + t st + (h / div) d + j, d the role's width.
@@ -46,6 +47,7 @@ struct LaParams {
   const int32_t* lens;   // or null
   int64_t L;
   int B, H;
+  int chunk;             // tokens per chunk: segments are whole chunks
   int nseg, cps;         // segments per sequence, chunks per segment
   int balanced;          // tensor cores: all chunks dealt to the CTAs in equal shares, cutting sequences
   int* hand_flags;       // balanced: per CTA, zeroed before the launch
@@ -65,7 +67,7 @@ __device__ __forceinline__ int64_t la_len(const LaParams& p, int b) {
 // Chunks [c0, c1) of segment `seg`, in natural order (a reverse role walks them from c1 - 1 down and
 // counts its segments from the sequence's end).
 __device__ __forceinline__ void la_segment(const LaParams& p, int64_t len, int seg, int rev, int& c0, int& c1) {
-  const int nch = (int)((len + kLaChunk - 1) / kLaChunk);
+  const int nch = (int)((uint32_t)(len + p.chunk - 1) / (uint32_t)p.chunk);
   const int a = (int)min((int64_t)nch, (int64_t)seg * p.cps), z = min(nch, a + p.cps);
   c0 = rev ? nch - z : a;
   c1 = rev ? nch - a : z;

@@ -71,15 +71,9 @@ __device__ __forceinline__ void store8(void* base, int64_t at, const float (&v)[
   }
 }
 
-// 1 / (1 + e^-z) with the exp2 and reciprocal instructions (each within 2^-22).
-__device__ __forceinline__ float sigmoid(float z) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(-kLog2e * z)));
-  return r;
-}
-
 // Two floats in one 64-bit register pair: the packed fp32 instructions round each as the scalar ones do and
-// take half the issue slots, which bound the backward.
+// take half the issue slots, which bound the backward (439 -> 391 us; the forward, which memory bounds, is
+// faster with scalar ones: 240 against 267 us).
 struct F2 {
   unsigned long long v;
 };
@@ -107,6 +101,12 @@ __device__ __forceinline__ F2 operator+(F2 a, F2 b) {
 __device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
   F2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+// 1 / (1 + e^-z) with the exp2 and reciprocal instructions (each within 2^-22).
+__device__ __forceinline__ float f_sigmoid(float z) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(-kLog2e * z)));
   return r;
 }
 __device__ __forceinline__ F2 f2_sigmoid(F2 z) {
@@ -329,10 +329,9 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) norm_fwd_kernel(con
   }
   uint32_t st = 0;
   int red_row = 0;
-  int64_t ahead = (first + (STAGES - 1) * step) * p.width;
   for (int64_t row = first; row < p.rows; row += step) {
-    in.fetch(row + (STAGES - 1) * step, p.rows, ahead, st == 0 ? STAGES - 1 : st - 1);
-    ahead += step * p.width;
+    const int64_t next = row + (STAGES - 1) * step;
+    in.fetch(next, p.rows, next * p.width, st == 0 ? STAGES - 1 : st - 1);
     in.use(row, st);
     if (++st == STAGES) st = 0;
     float a[NV][8];
@@ -348,7 +347,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) norm_fwd_kernel(con
         float z[8];
         in.template get<1>(i, z);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[i][e] *= z[e] * sigmoid(z[e]);
+        for (int e = 0; e < 8; ++e) a[i][e] *= z[e] * f_sigmoid(z[e]);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) s[i] = fmaf(a[i][e], a[i][e], s[i]);
@@ -376,7 +375,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) norm_fwd_kernel(con
         float z[8];
         in.template get<1>(i, z);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[i][e] *= z[e] * sigmoid(z[e]);
+        for (int e = 0; e < 8; ++e) a[i][e] *= z[e] * f_sigmoid(z[e]);
       }
       float r[8];
       if (p.res) in.template get<2>(i, r);
