@@ -21,8 +21,8 @@
 //   warps 12-15  one column c of M each, in fp32 registers for the whole item: M's bf16 copy for the
 //                readout (the only rounding of M), M <- γ^n M + U. (U is summed apart from M: the tensor
 //                cores' own accumulation would lose a little of M at every step.)
-//   warps 16-23  (γ w)ᵀ as three bf16 parts into tensor memory (a ring of 16-token steps, dealt in turn to
-//                two sets of four warps)
+//   warps 16-23  (γ w)ᵀ as three bf16 parts into tensor memory (a ring of 16- or 32-token slots, filled
+//                by two sets of four warps)
 // Except for M's columns all loops stay rolled: six kinds of warps share the instruction cache, whose misses
 // go to a cache that the SMs of a cluster share in their turn. With every loop unrolled, a chunk took a
 // quarter longer on SMs with 15 neighbours at work than on those with few.
@@ -35,7 +35,7 @@
 // Rounded to bf16: P and M's copy, once each, because each meets a bf16 operand and makes a bf16
 // output; γ w enters M as hi + mid + lo, 24 bits together, where M is an output, so that it stays an fp32
 // state (two parts would put 3e-6 into S_final and dS0, three 1e-7); else as hi + mid.
-// Tensor memory: scores / P 128 columns, out 128, U dx, the γ w ring 96.
+// Tensor memory: scores / P 128 columns, out dw, U dx, the γ w ring 96 or 192.
 // P's tokens 0-63 lie in columns 0-31, tokens 64-127 in columns 64-95: where the same warp has read scores.
 // Every wait is bounded; a wait that runs out records SWIMBA_ERR_TIMEOUT, and the CTA drains and exits.
 #include <cuda.h>
@@ -76,13 +76,15 @@ enum { kMapX, kMapY, kMapW, kMapOut };
 template <int DX, int DW, int MODE>
 struct LaSmem {
   static constexpr int XB = DX / 64, WB = DW / 64;
-  // Without scores and outputs there is room for two U and a longer ring, and the warps that would make
-  // them fill it too.
-  // A slot of the ring is one MMA step where columns are short, so that it is refilled in half the time, and
-  // two where there are enough: an issuing warp spends about 300 cycles on a slot, three MMAs take 192.
-  static constexpr int NU = MODE == 0 ? 1 : 2, RING = 4, SETS = MODE == 0 ? 2 : 4, SUB = MODE == 0 ? 1 : 2;
-  static constexpr int SLOTS = kLaChunk / (kStep * SUB);  // per chunk
-  static constexpr uint32_t COL_U = MODE == 0 ? 256 : 0, COL_RING = MODE == 0 ? 384 : 256;
+  // The ring's slots are 32 tokens, two MMA steps, each filled by one set of warps: the issuing warp spends
+  // about 450 cycles on a slot beside its MMAs, and a set about 500 on a step. Only four slots fit where
+  // both sizes are 128; there they are 16 tokens (two of 32 were 2 % slower). Without scores and outputs
+  // there is room for two U, and the warps that would make them fill the ring too.
+  static constexpr int NU = MODE == 0 ? 1 : 2, RING = 4, SUB = MODE == 0 && DX + DW == 256 ? 1 : 2;
+  static constexpr int GROUPS = (MODE == 0 ? 2 : 4) / SUB;  // SUB sets fill a slot, GROUPS slots are filled at a time
+  static constexpr int SLOTS = kLaChunk / (kStep * SUB);     // per chunk
+  static constexpr uint32_t COL_U = MODE == 0 ? kColO + DW : 0, COL_RING = MODE == 0 ? COL_U + DX : 256;
+  static_assert(COL_RING + RING * SUB * 3 * kPart <= 512, "tensor memory");
   static constexpr int TX = MODE == 0 ? XB * kTile : 0, TY = XB * kTile, TW = WB * kTile;  // one tile of each
   static constexpr int COPY = MODE == 0 ? DX * DW * 2 : 0;  // M's bf16 copy, [dw rows][dx], K-major
   // Tiles in flight. An X tile is free after two MMAs, a Y tile after U, a W tile only when the outputs
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     mbar_init(o_full, 1);
     mbar_init(o_free, 8);
     for (int i = 0; i < SM::RING; ++i) {
-      mbar_init(&ring_full[i], 4);
+      mbar_init(&ring_full[i], 4 * SM::SUB);
       mbar_init(&ring_empty[i], 1);
     }
     for (int i = 0; i < SM::NU; ++i) {
@@ -726,48 +728,45 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         // holds channel t / 4 of tokens 2 (t % 4) + 0..1, scaled, split and stored in that form
         const uint32_t tw = smem_u32(sm) + SM::W + st * SM::TW + (wq >> 1) * kTile + ((lane & 7) + 8 * (lane >> 4)) * 128;
 #pragma unroll 1
-        for (int k = set; k < SM::SLOTS; k += SM::SETS) {
+        for (int k = set / SM::SUB; k < SM::SLOTS; k += SM::GROUPS) {
           constexpr int R = SM::RING, PER = SM::SLOTS / R;
           const uint32_t slot = k % R;
           if (!(ok = wait(&ring_empty[slot], ((it * PER + k / R) & 1) ^ 1))) break;
           tc_fence_after();
           if (active) {
-#pragma unroll 1
-            for (int sub = 0; sub < SM::SUB; ++sub) {
-              const int step = k * SM::SUB + sub;
-              uint32_t raw[2][4];
+            const int sub = set % SM::SUB, step = k * SM::SUB + sub;
+            uint32_t raw[2][4];
 #pragma unroll
-              for (int half = 0; half < 2; ++half)  // 16 channels: matrices (tokens, channels) (0, 0), (0, 8), (8, 0), (8, 8)
-                ldmatrix_x4_trans(tw + step * (kStep * 128) + ((((wq & 1) * 4 + half * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4),
-                                  raw[half]);
-              float2 wt[2];
-              uint32_t keep[2];
+            for (int half = 0; half < 2; ++half)  // 16 channels: matrices (tokens, channels) (0, 0), (0, 8), (8, 0), (8, 8)
+              ldmatrix_x4_trans(tw + step * (kStep * 128) + ((((wq & 1) * 4 + half * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4),
+                                raw[half]);
+            float2 wt[2];
+            uint32_t keep[2];
 #pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                // γ^(n-1-s), reverse γ γ^s; tokens behind the last chunk's end count as zeros whatever they hold
-                const int s = kStep * step + 8 * g + 2 * (lane & 3), e = rev ? s : max(n - 2 - s, -1);
-                const float a0 = lds1(table + (rev ? -e : e + 1) * 4), a1 = lds1(table + (rev ? -e - 1 : e) * 4);
-                wt[g] = make_float2(a0 * f_w, a1 * f_w);
-                keep[g] = (s < n ? 0xffffu : 0u) | (s + 1 < n ? 0xffff0000u : 0u);
+            for (int g = 0; g < 2; ++g) {
+              // γ^(n-1-s), reverse γ γ^s; tokens behind the last chunk's end count as zeros whatever they hold
+              const int s = kStep * step + 8 * g + 2 * (lane & 3), e = rev ? s : max(n - 2 - s, -1);
+              const float a0 = lds1(table + (rev ? -e : e + 1) * 4), a1 = lds1(table + (rev ? -e - 1 : e) * 4);
+              wt[g] = make_float2(a0 * f_w, a1 * f_w);
+              keep[g] = (s < n ? 0xffffu : 0u) | (s + 1 < n ? 0xffff0000u : 0u);
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+              for (int d = 0; d < 4; ++d) {
+                // three truncated parts of 8 bits each: their sum is the product's 24 bits
+                const uint32_t v = raw[half][d] & keep[d >> 1];
+                const float v0 = bf16lo(v) * wt[d >> 1].x, v1 = bf16hi(v) * wt[d >> 1].y;
+                hi[d] = high_halves(v0, v1);
+                const float r0 = v0 - top_bits(v0), r1 = v1 - top_bits(v1);
+                mid[d] = high_halves(r0, r1);
+                lo[d] = high_halves(r0 - top_bits(r0), r1 - top_bits(r1));
               }
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                uint32_t hi[4], mid[4], lo[4];
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                  // three truncated parts of 8 bits each: their sum is the product's 24 bits
-                  const uint32_t v = raw[half][d] & keep[d >> 1];
-                  const float v0 = bf16lo(v) * wt[d >> 1].x, v1 = bf16hi(v) * wt[d >> 1].y;
-                  hi[d] = high_halves(v0, v1);
-                  const float r0 = v0 - top_bits(v0), r1 = v1 - top_bits(v1);
-                  mid[d] = high_halves(r0, r1);
-                  lo[d] = high_halves(r0 - top_bits(r0), r1 - top_bits(r1));
-                }
-                const uint32_t at = tl + ((uint32_t)(16 * half) << 16) + SM::COL_RING + (slot * SM::SUB + sub) * 3 * kPart;
-                tmem_st_16x128b_x2(at, hi);
-                tmem_st_16x128b_x2(at + kPart, mid);
-                if (t.parts == 3) tmem_st_16x128b_x2(at + 2 * kPart, lo);
-              }
+              const uint32_t at = tl + ((uint32_t)(16 * half) << 16) + SM::COL_RING + (slot * SM::SUB + sub) * 3 * kPart;
+              tmem_st_16x128b_x2(at, hi);
+              tmem_st_16x128b_x2(at + kPart, mid);
+              if (t.parts == 3) tmem_st_16x128b_x2(at + 2 * kPart, lo);
             }
             tmem_wait_st();
           }
