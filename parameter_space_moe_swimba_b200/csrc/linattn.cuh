@@ -37,7 +37,7 @@ struct LaRole {
   float* M_end;          // likewise
   int sj, sc;
   float* seg;            // [B H, nseg, dx, dw] segment states, or null (one segment)
-  int parts;             // bf16 parts of the weighted values: 3 where M itself is an output, else 2
+  int parts;             // bf16 parts of the weighted values, at most: 3 where M itself is an output, else 2
 };
 
 struct LaParams {

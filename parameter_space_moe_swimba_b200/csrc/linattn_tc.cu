@@ -33,8 +33,9 @@
 // (256 sequences and heads on 148 CTAs: 56 chunks per CTA in place of 64.)
 //
 // Rounded to bf16: P and M's copy, once each, because each meets a bf16 operand and makes a bf16
-// output; γ w enters M as hi + mid + lo, 24 bits together, where M is an output, so that it stays an fp32
-// state (two parts would put 3e-6 into S_final and dS0, three 1e-7); else as hi + mid.
+// output; γ w enters M as hi + mid + lo, 24 bits together, where it matters to an fp32 state: where M is
+// an output and the chunk's decay to the sequence's end is more than 2^-6; else as hi + mid, 16 bits (all
+// through, they would put 3e-6 into S_final and dS0; so they put 1e-7).
 // Tensor memory: scores / P 128 columns, out dw, U dx, the γ w ring 96 or 192.
 // P's tokens 0-63 lie in columns 0-31, tokens 64-127 in columns 64-95: where the same warp has read scores.
 // Every wait is bounded; a wait that runs out records SWIMBA_ERR_TIMEOUT, and the CTA drains and exits.
@@ -96,6 +97,11 @@ struct LaSmem {
   static constexpr int NBAR = 2 * NX + 2 * NY + 4 * NW + 6 + 2 * RING + 2 * NU + 4 + 2 + 2;
   static constexpr int MISC = BAR + NBAR * 8;
   static constexpr int BYTES = MISC + 16;
+  // Registers per thread of the six warpgroups (0-3, 4-7 and 8-11, 12-15, 16-19 and 20-23). A spill in one of
+  // the chunk loops costs several percent.
+  static constexpr int REG_UTIL = DX == 128 ? 48 : DW == 128 ? 72 : 48, REG_PO = DX == 128 ? 64 : DW == 128 ? 72 : 80,
+                       REG_M = DX == 128 ? 176 : DW == 128 ? 120 : 144, REG_W = DX == 128 ? 64 : DW == 128 ? 72 : 64;
+  static_assert(REG_UTIL + 2 * REG_PO + REG_M + 2 * REG_W <= 6 * 80, "what the launch's 80 registers per thread allow");
   static_assert(BYTES + 1024 <= 232448, "shared memory of one CTA");
 };
 
@@ -141,8 +147,9 @@ __device__ __forceinline__ float top_bits(float v) { return __uint_as_float(__fl
 struct LaItem {
   const LaRole* r;  // in the kernel's parameters: what a chunk's loop uses is copied out first, since behind
                     // every asm statement it would be loaded again, through memory
-  int role, b, h, seg, c0, c1, rev, parts;
-  int64_t bh, len;
+  int role, b, h, seg, c0, c1, rev, len;
+  int third;  // γ w's third part counts where at most so many tokens follow (-1: nowhere)
+  int64_t bh;
   bool begins, ends;  // the state before it is given (else handed over); the state after it is the end's (else to be handed over)
 };
 
@@ -179,8 +186,9 @@ __device__ __forceinline__ bool la_item(const LaTcArgs& a, uint32_t k, LaItem& t
   t.b = (int)(bh / (uint32_t)p.H);
   t.h = (int)bh - t.b * p.H;
   t.rev = t.r->rev;
-  t.parts = t.r->parts;
-  t.len = la_len(p, t.b);
+  // γ^tokens > 2^-6
+  t.third = t.r->parts < 3 ? -1 : (int)fminf(__fdividef(6.f, fabsf(p.g[t.h]) * kLog2e), 2e9f);
+  t.len = (int)la_len(p, t.b);  // at most 2^30
   la_segment(p, t.len, t.seg, t.rev, t.c0, t.c1);
   t.begins = p0 == 0;
   t.ends = p1 == 0xffffffffu;
@@ -206,10 +214,15 @@ __device__ __forceinline__ bool hand_wait(int* flag, volatile int* abort, int la
   __threadfence();
   return true;
 }
+// Whether the chunk [t0, t0 + n) needs all three parts.
+__device__ __forceinline__ bool la_third(const LaItem& t, int t0, int n) {
+  return (t.rev ? t0 : t.len - t0 - n) <= t.third;
+}
+
 // First token of the item's chunk number `i` and its count.
-__device__ __forceinline__ int la_chunk(const LaItem& t, int i, int64_t& t0) {
-  t0 = (int64_t)(t.rev ? t.c1 - 1 - i : t.c0 + i) * kLaChunk;
-  return (int)min((int64_t)kLaChunk, t.len - t0);
+__device__ __forceinline__ int la_chunk(const LaItem& t, int i, int& t0) {
+  t0 = (t.rev ? t.c1 - 1 - i : t.c0 + i) * kLaChunk;
+  return min(kLaChunk, t.len - t0);
 }
 
 }  // namespace
@@ -296,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
   };
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SM::REG_UTIL));
     if (warp == 0) {
       // ---------------- loads ----------------
       uint32_t it = 0, ii = 0;
@@ -316,11 +329,11 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           if (lane == 0) mbar_arrive(&pw_full[ii & 1]);
         }
         for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
-          int64_t t0;
+          int t0;
           la_chunk(t, i, t0);
           auto load = [&](int boxes, int at, const CUtensorMap* m, uint64_t* bar, int head) {
             mbar_arrive_expect_tx(bar, boxes * kTile);
-            for (int k = 0; k < boxes; ++k) tma_load_4d(sm + at + k * kTile, m, bar, 64 * k, head, (int)t0, t.b);
+            for (int k = 0; k < boxes; ++k) tma_load_4d(sm + at + k * kTile, m, bar, 64 * k, head, t0, t.b);
           };
           // in the order in which the tiles come free
           if (!(ok = wait(&w_empty[it % NW], ((it / NW) & 1) ^ 1))) break;
@@ -361,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       for (LaItem t; ok && la_item(a, ii, t); ++ii) {
         for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
           const uint32_t ph = it & 1;
-          int64_t t0;
+          int t0;
           const int n = la_chunk(t, i, t0);
           const uint32_t sX = (base + SM::X + (it % NX) * SM::TX) >> 4, sY = (base + SM::Y + (it % NY) * SM::TY) >> 4,
                          sW = (base + SM::W + (it % NW) * SM::TW) >> 4;
@@ -389,6 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
             }
             // U = Σ_s (γ w_s) y_sᵀ, 16 tokens at a time
             const uint32_t ub = it % SM::NU, up = (it / SM::NU) & 1;
+            const bool third = la_third(t, t0, n);
             if (!(ok = wait(&u_free[ub], up ^ 1))) break;
             // A poll queues up behind the MMAs issued before it; asked for after them, it left the tensor cores
             // about 140 cycles without work at every step. So each step's is issued before the MMAs of the
@@ -405,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                 for (int sub = 0; sub < SM::SUB; ++sub)
 #pragma unroll
                   for (int part = 0; part < 3; ++part)
-                    if (part < 2 || t.parts == 3)
+                    if (part < 2 || third)
                       mma_bf16_ts(tmem + SM::COL_U + ub * 128,
                                   tmem + SM::COL_RING + ((k % R) * SM::SUB + sub) * 3 * kPart + part * kPart,
                                   dMN + sY + (k * SM::SUB + sub) * (kStep * 8), id_u, (k | sub | part) != 0);
@@ -477,14 +491,14 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           const bool out_f32 = t.r->out_f32 != 0;
           for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
             const int st = it % NW;
-            int64_t t0;
+            int t0;
             const int n = la_chunk(t, i, t0);
             if (!(ok = wait(&staged[st], (it / NW) & 1))) break;
             if (elect_one()) {
               if (!out_f32 && (n == kLaChunk || t0 + n == p.L)) {
 #pragma unroll
                 for (int k = 0; k < SM::WB; ++k)
-                  tma_store_4d(&a.map[t.role][kMapOut], sm + SM::W + st * SM::TW + k * kTile, 64 * k, t.h, (int)t0, t.b);
+                  tma_store_4d(&a.map[t.role][kMapOut], sm + SM::W + st * SM::TW + k * kTile, 64 * k, t.h, t0, t.b);
                 bulk_commit();
                 bulk_wait_read<0>();
               }
@@ -499,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       }
     }
   } else if (MODE == 0 && warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SM::REG_PO));
     {
       // ---------------- scores -> P, outputs ----------------
       const int wq = warp & 3, set = (warp >> 2) - 1, row = 32 * wq + lane;
@@ -511,15 +525,13 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         const int rev = t.rev;
         const uint32_t table = smem_u32(sm) + SM::POW + ((ii & 1) * kTable + la_origin(rev) + row) * 4;
         const float s_inter = r.s_inter, s_intra = s_inter * r.s_u, lg = p.g[t.h] * kLog2e;
-        const int out_f32 = r.out_f32, dw = r.dw;
-        const int64_t out_st = r.out_st, out_bh = t.b * r.out_sb + (int64_t)t.h * dw;
-        void* const out = r.out;
+        const bool out_f32 = r.out_f32 != 0;
         const float f_all = s_inter * la_pow(lg, rev ? kLaChunk - 1 - row : row + 1);
         if (!(ok = wait(&pw_full[ii & 1], (ii >> 1) & 1))) break;
         for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
           const int st = it % NW;
           const uint32_t ph = it & 1;
-          int64_t t0;
+          int t0;
           const int n = la_chunk(t, i, t0);
           if (!(ok = wait(sc_full, ph))) break;
           tc_fence_after();
@@ -565,7 +577,6 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           tc_fence_after();
           const uint32_t tile = smem_u32(sm) + SM::W + st * SM::TW;
           const bool whole = !out_f32 && (n == kLaChunk || t0 + n == p.L);
-          const int64_t at = out_bh + (t0 + row) * out_st;
 #pragma unroll 1
           for (int k = 0; k < DW / 64; ++k) {
             float f[32];
@@ -577,6 +588,9 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
                 sts4(tile + (b32 >> 1) * kTile + swz16(row, (b32 & 1) * 4 + c), pair(f[8 * c], f[8 * c + 1]),
                      pair(f[8 * c + 2], f[8 * c + 3]), pair(f[8 * c + 4], f[8 * c + 5]), pair(f[8 * c + 6], f[8 * c + 7]));
             } else if (row < n) {
+              const int dw = r.dw;
+              void* const out = r.out;
+              const int64_t at = t.b * r.out_sb + (t0 + row) * r.out_st + (int64_t)t.h * dw;
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 const int col = b32 * 32 + 8 * c;
@@ -609,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       if (!ok) give_up(75);
     }
   } else if (warp >= 12 && warp < 16) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SM::REG_M));
     // ---------------- the state ----------------
     const int wq = warp & 3, col = 32 * wq + lane;  // column of M = lane of U
     const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16);
@@ -659,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           if (it > 0 && !(ok = wait(mx_full, (it & 1) ^ 1))) break;
           copy();
         }
-        int64_t t0;
+        int t0;
         const int n = la_chunk(t, i, t0);
         const float g = n == kLaChunk ? g_all : la_pow(lg, n);
         const uint32_t ub = it % SM::NU;
@@ -671,11 +685,11 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         }
         if (active) {
 #pragma unroll
-          for (int k = 0; k < DX / 32; ++k) {
-            float f[32];
-            tmem_ld32(tl + SM::COL_U + ub * 128 + k * 32, f);
+          for (int k = 0; k < DX / 16; ++k) {
+            float f[16];
+            tmem_ld16(tl + SM::COL_U + ub * 128 + k * 16, f);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) m[k * 32 + j] = fmaf(g, m[k * 32 + j], f[j]);
+            for (int j = 0; j < 16; ++j) m[k * 16 + j] = fmaf(g, m[k * 16 + j], f[j]);
           }
         }
         tc_fence_before();
@@ -700,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     }
     if (!ok) give_up(76);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SM::REG_W));
     // ---------------- (γ w)ᵀ ----------------
     const int wq = warp & 3;
     const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16);
@@ -721,8 +735,9 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
       if (!(ok = wait(&pw_full[ii & 1], (ii >> 1) & 1))) break;
       for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
         const int st = it % NW;
-        int64_t t0;
+        int t0;
         const int n = la_chunk(t, i, t0);
+        const bool third = la_third(t, t0, n);
         if (!(ok = wait(&w_full[st], (it / NW) & 1))) break;
         // 16 tokens at a time: 8 x 8 blocks of W, transposed on the way to the registers, where thread t
         // holds channel t / 4 of tokens 2 (t % 4) + 0..1, scaled, split and stored in that form
@@ -766,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
               const uint32_t at = tl + ((uint32_t)(16 * half) << 16) + SM::COL_RING + (slot * SM::SUB + sub) * 3 * kPart;
               tmem_st_16x128b_x2(at, hi);
               tmem_st_16x128b_x2(at + kPart, mid);
-              if (t.parts == 3) tmem_st_16x128b_x2(at + 2 * kPart, lo);
+              if (third) tmem_st_16x128b_x2(at + 2 * kPart, lo);
             }
             tmem_wait_st();
           }
