@@ -329,7 +329,7 @@ LaPlan la_plan(const swimba_linattn_dims* d, int roles, bool tc) {
   const int64_t heads = d->batch * d->n_heads * roles * (tc ? 1 : (std::max(d->d_k, d->d_v) + kSimtCols - 1) / kSimtCols);
   const int64_t slots = tc ? kSMs : 4 * kSMs;
   const double pass = tc ? 0.5 : 0.7, state = tc ? 2 : 0.3, launch = tc ? 4 : 0.7;
-  LaPlan best{tc, 1, (int)nch, tc};
+  LaPlan best{tc, 1, (int)nch, tc && heads >= kSMs};
   double least = (double)((heads + slots - 1) / slots) * nch;
   for (int64_t n = 2; n <= std::min<int64_t>(nch, 64); ++n) {
     const int64_t cps = (nch + n - 1) / n, segs = (nch + cps - 1) / cps;
