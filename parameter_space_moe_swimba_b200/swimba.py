@@ -262,23 +262,33 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
-def _pointers(*tensors):
-    """Device pointers of a call's tensors, or None where one lies on another device than the current one,
-    whose stream the call would use."""
-    device, out = torch.cuda.current_device() if torch.cuda.is_initialized() else -1, []
-    for t in tensors:
+def _same_places(t, st, lay, dims) -> bool:
+    """Whether strides that differ from `lay` still name the same elements: an axis of one has none."""
+    return (len(st) == 4 and (st[0] == lay[0] or dims.batch == 1) and (st[1] == lay[1] or dims.seqlen == 1)
+            and (st[2] == lay[2] or t.shape[2] == 1) and (st[3] == 1 or t.shape[3] == 1))
+
+
+def _pointers(dense, dims=None, strided=()):
+    """Device pointers of a call's tensors: [B, L, heads, d] ones, each with the token stride that the call's
+    dims state for it, then those that have to be dense. None where one is laid out differently or lies on
+    another device than the current one, whose stream the call would use (a CPU tensor's is -1, no device yet
+    -2). Integers are taken as pointers and not looked at."""
+    device = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    out = []
+    for t, stride, d in strided:
         if isinstance(t, torch.Tensor):
-            if t.get_device() != device:
+            lay, st = (dims.seqlen * stride, stride, d, 1), t.stride()
+            if t.get_device() != device or (st != lay and not _same_places(t, st, lay, dims)):
                 return None
-            out.append(t.data_ptr())
-        else:
-            out.append(t)
+            t = t.data_ptr()
+        out.append(t)
+    for t in dense:
+        if isinstance(t, torch.Tensor):
+            if t.get_device() != device or not t.is_contiguous():
+                return None
+            t = t.data_ptr()
+        out.append(t)
     return out
-
-
-def _lies_as(stride, t) -> bool:
-    """Whether a gradient [B, L, heads, d] has its input's token stride."""
-    return not isinstance(t, torch.Tensor) or t.shape[1] == 1 or t.stride(1) == stride
 
 
 def check(status: int, where: str = "swimba") -> None:
@@ -447,24 +457,30 @@ def swimba_linattn_workspace_size(dims: swimba_linattn_dims, op: int) -> int:
 
 
 def swimba_linattn_fwd(dims, q, k, v, log_decay, lens, S0, o, S_final, ws, ws_bytes, stream=None) -> int:
-    p = _pointers(q, k, v, log_decay, lens, S0, o, S_final, ws)
+    p = _pointers((log_decay, lens, S0, o, S_final, ws), dims,
+                  ((q, dims.q_stride, dims.d_k), (k, dims.k_stride, dims.d_k), (v, dims.v_stride, dims.d_v)))
     return 1 if p is None else _lib.swimba_linattn_fwd(ctypes.byref(dims), *p, ws_bytes, _stream(stream))
 
 
 def swimba_linattn_step(dims, q, k, v, log_decay, S_in, o, S_out, stream=None) -> int:
-    p = _pointers(q, k, v, log_decay, S_in, o, S_out)
+    p = _pointers((log_decay, S_in, o, S_out), dims,
+                  ((q, dims.q_stride, dims.d_k), (k, dims.k_stride, dims.d_k), (v, dims.v_stride, dims.d_v)))
     return 1 if p is None else _lib.swimba_linattn_step(ctypes.byref(dims), *p, _stream(stream))
 
 
 def swimba_linattn_bwd(dims, q, k, v, log_decay, lens, S0, g_o, g_S, dq, dk, dv, dS0, ws, ws_bytes, stream=None) -> int:
-    p = _pointers(q, k, v, log_decay, lens, S0, g_o, g_S, dq, dk, dv, dS0, ws)
-    if p is None or not (_lies_as(dims.q_stride, dq) and _lies_as(dims.k_stride, dk) and _lies_as(dims.v_stride, dv)):
+    ql, kl, vl = (dims.q_stride, dims.d_k), (dims.k_stride, dims.d_k), (dims.v_stride, dims.d_v)
+    p = _pointers((log_decay, lens, S0, g_o, g_S, dS0, ws), dims,
+                  ((q, *ql), (k, *kl), (v, *vl), (dq, *ql), (dk, *kl), (dv, *vl)))
+    if p is None:
         return 1
-    return _lib.swimba_linattn_bwd(ctypes.byref(dims), *p, ws_bytes, _stream(stream))
+    q, k, v, dq, dk, dv, log_decay, lens, S0, g_o, g_S, dS0, ws = p
+    return _lib.swimba_linattn_bwd(ctypes.byref(dims), q, k, v, log_decay, lens, S0, g_o, g_S, dq, dk, dv, dS0, ws,
+                                   ws_bytes, _stream(stream))
 
 
 def swimba_block_norm_fwd(dims, y, z, w_post, res, w_pre, h, n, stream=None) -> int:
-    p = _pointers(y, z, w_post, res, w_pre, h, n)
+    p = _pointers((y, z, w_post, res, w_pre, h, n))
     return 1 if p is None else _lib.swimba_block_norm_fwd(ctypes.byref(dims), *p, _stream(stream))
 
 
@@ -474,7 +490,7 @@ def swimba_block_norm_workspace_size(dims: swimba_norm_dims) -> int:
 
 def swimba_block_norm_bwd(dims, y, z, w_post, res, w_pre, g_h, g_n, dy, dz, dres, dw_post, dw_pre, ws, ws_bytes,
                           stream=None) -> int:
-    p = _pointers(y, z, w_post, res, w_pre, g_h, g_n, dy, dz, dres, dw_post, dw_pre, ws)
+    p = _pointers((y, z, w_post, res, w_pre, g_h, g_n, dy, dz, dres, dw_post, dw_pre, ws))
     return 1 if p is None else _lib.swimba_block_norm_bwd(ctypes.byref(dims), *p, ws_bytes, _stream(stream))
 
 

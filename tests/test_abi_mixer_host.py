@@ -71,6 +71,9 @@ def test_linattn_arguments(S):
     d = la_dims(S)
     need = S.swimba_linattn_workspace_size(d, S.SWIMBA_OP_LINATTN_FWD)
     assert need >= 256 and S.swimba_linattn_workspace_size(d, S.SWIMBA_OP_LINATTN_FWD + 5) == 0
+    # few heads need no room for states handed from CTA to CTA, many do
+    many = la_dims(S, batch=64)
+    assert need < 4096 and S.swimba_linattn_workspace_size(many, S.SWIMBA_OP_LINATTN_FWD) >= 148 * 65536
     for x in ("q", "k", "v", "g", "o"):
         assert fwd(S, d, **{x: None}) == INVALID
     for x in ("q", "k", "v", "o", "S0", "S_final", "ws"):
@@ -114,10 +117,33 @@ def test_linattn_layouts(S):
                 (q[:, ::2], k[:, ::2], v[:, ::2])):
         with pytest.raises(S.SwimbaError):
             S.make_linattn_dims(*bad, 1.0)
-    # gradients have to lie as their inputs do; CPU tensors are on another device than the call's
-    dense = torch.zeros(2, 5, 4, 16)
+    # CPU tensors are on another device than a call's
+    state, o = torch.zeros(2, 4, 16, 16), torch.zeros(2, 5, 4, 16)
+    d = S.make_linattn_dims(o, o, o, 0.5)
+    assert S.swimba_linattn_fwd(d, o, o, o, FAKE, None, state, FAKE + 4096, state, FAKE, 1 << 40, 0) == INVALID
+
+
+def test_tensors_lie_as_the_dims_say(S, monkeypatch):
+    """Inputs and gradients have the dims' token strides and the rest is dense; anything else is refused,
+    for it would be read as other elements. CPU tensors stand in for the device's: the device is named -1."""
+    monkeypatch.setattr(S.torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(S.torch.cuda, "current_device", lambda: -1)
+    buf = torch.zeros(2, 5, 4 * 16 + 2 * 16 + 2 * 16)
+    q, k, v = buf.split([64, 32, 32], dim=2)
+    q, k, v = q.unflatten(2, (4, 16)), k.unflatten(2, (2, 16)), v.unflatten(2, (2, 16))
     d = S.make_linattn_dims(q, k, v, 0.5)
-    assert not S._lies_as(d.q_stride, dense) and S._lies_as(d.q_stride, q)
+    lies = lambda dims, x, dense=(): S._pointers(dense, dims, ((x, dims.q_stride, dims.d_k),)) is not None
+    assert lies(d, q) and not lies(d, q.contiguous()) and not lies(d, torch.zeros(2, 4, 5, 16).transpose(1, 2))
+    state = torch.zeros(2, 4, 16, 16)
+    assert lies(d, q, (state, None, FAKE)) and not lies(d, q, (state.transpose(2, 3),))
+    # part of a longer buffer, heads apart, elements apart: the token stride alone would fit
+    assert not lies(d, torch.zeros(2, 6, 128)[:, :5, :64].unflatten(2, (4, 16)))
+    assert not lies(d, buf.unflatten(2, (4, 32))[..., :16])
+    assert not lies(d, buf.unflatten(2, (16, 8))[..., :4].transpose(2, 3))
+    # one token: the distance between sequences counts
+    d = S.make_linattn_dims(q[:, :1], k[:, :1], v[:, :1], 0.5)
+    assert d.q_stride == 5 * 128 and lies(d, q[:, :1]) and not lies(d, q[:, :1].contiguous())
+    assert lies(d, q[:1, :1].contiguous())
 
 
 def norm_dims(S, **kw):
