@@ -236,9 +236,10 @@ __global__ void __launch_bounds__(256) la_rows_kernel(IO* out, int64_t st, int64
 
 // ---- decode step ----------------------------------------------------------------------------------------
 // One CTA per (sequence, head) and `cols` columns: the state is read and written once (8 d_k d_v bytes),
-// which bounds it: 1 GiB of state in 189 us, 88 % of the measured copy rate. Threads go over the state row
-// by row, 16 bytes each; the partial readouts of the threads that share columns meet in shared memory.
-// Few heads are cut into 32 columns (128 bytes of a row), so that every SM has a share.
+// which bounds it: 512 MiB of state, bf16 tokens, in 164 us, the measured copy rate. Threads go over the state
+// row by row, 16 bytes each; the partial readouts of the threads that share columns meet in shared memory.
+// Few heads are cut into 32 columns (128 bytes of a row), so that every SM has a share: 96 heads of 128 x 128
+// take 4.1 us, 6.2 whole. Many heads stay whole, rows of 512 bytes; a call of a few heads is bound by its launch.
 template <typename IO>
 __global__ void __launch_bounds__(256) la_step_kernel(LaStream q, LaStream k, LaStream v, const float* g,
                                                       const float* S_in, IO* o, float* S_out, int H, int dk, int dv,
@@ -321,8 +322,8 @@ swimba_status check_la(const swimba_linattn_dims* d) {
 // least time in units of one chunk's outputs on one CTA: rounds of CTAs x chunks per segment, with
 // `pass` units more per chunk for the state pass of a split sequence, `state` per segment for its
 // state's way through memory and `launch` for the two launches more. Tensor cores (a unit is about 3 us):
-// 16 heads x 65536 tokens take 0.36 ms in 9 segments, 2.1 ms whole. fp32 (32 tokens, 8 us): 48 roles x
-// 333 tokens take 76 us in segments, 176 us whole.
+// 16 heads x 65536 tokens take 0.39 ms in 9 segments, 2.1 ms whole. fp32 (32 tokens, 8 us): 48 roles x
+// 333 tokens take 76 us in segments, 176 us whole. Fewer heads than SMs are never cut between two CTAs.
 LaPlan la_plan(const swimba_linattn_dims* d, int roles, bool tc) {
   const int chunk = tc ? kLaChunk : kLaSimtChunk;
   const int64_t nch = (d->seqlen + chunk - 1) / chunk;

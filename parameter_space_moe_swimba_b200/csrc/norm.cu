@@ -18,7 +18,9 @@
 // its own (cp.async, no barrier), two rows ahead, and keeps its channels' weights and their gradients in
 // registers. Without the copies a row's loads waited for the row before it (16384 rows of 4096, bf16
 // with an fp32 residual, backward: 547 us, 2.7 TB/s); with 8 channels per thread a third of the
-// instructions were the row's sums and addresses, so a thread takes 16 where rows are long.
+// instructions were the row's sums and addresses, so a thread takes 16 where rows are long. Now that backward
+// takes 400 us (3.7 TB/s, 57 % of the measured copy rate: its 5 block-wide sums per row and 90 registers of
+// state leave two CTAs of 8 warps per SM to hide them), the forward of 32768 rows of 4096 in bf16 228 us (90 %).
 // All sums are fp32 and taken in a fixed order.
 #include <algorithm>
 #include <type_traits>

@@ -171,3 +171,23 @@ def test_in_place_outputs_repeats_and_graphs(S):
     torch.cuda.synchronize()
     assert all(torch.equal(out[k], grads[k]) for k in out)
     del graph
+
+
+def test_offsets_past_32_bits(S):
+    """Rows more than 2^31 elements in give the bits that they give as the first rows."""
+    rows, width = 2 ** 18 + 40, 8192
+    if torch.cuda.mem_get_info()[0] < 28 << 30:
+        pytest.skip("needs 18 GB of device memory")
+    c = Case(9, 50, width, groups=2, z=False, res=False)
+    h, n = c.forward(S)
+    back = c.backward(S)
+    big = Case(9, 50, width, groups=2, z=False, res=False)
+    big.rows = rows
+    big.y, big.g_h, big.g_n = (torch.zeros(rows, width, device="cuda", dtype=x.dtype) for x in (c.y, c.g_h, c.g_n))
+    for x, part in ((big.y, c.y), (big.g_h, c.g_h), (big.g_n, c.g_n)):
+        x[-50:] = part
+    got_h, got_n = big.forward(S)
+    assert torch.equal(got_h[-50:], h) and torch.equal(got_n[-50:], n) and not got_n[:-50].any()
+    del got_h, got_n
+    dy = big.backward(S)["dy"]
+    assert torch.equal(dy[-50:], back["dy"]) and not dy[:-50].any()
