@@ -15,12 +15,13 @@
 // Bound by memory: every tensor is read or written once, 16 bytes per thread and access. A row belongs to
 // one warp (up to 256 channels) or one CTA of up to 512 threads, which walks its rows with the next ones
 // on their way: each thread copies the vectors of 8 channels that it will work on into shared memory of
-// its own (cp.async, no barrier), two rows ahead, and keeps its channels' weights and their gradients in
+// its own (cp.async, no barrier), as many rows ahead as fit, and keeps its channels' weights and their gradients in
 // registers. Without the copies a row's loads waited for the row before it (16384 rows of 4096, bf16
 // with an fp32 residual, backward: 547 us, 2.7 TB/s); with 8 channels per thread a third of the
 // instructions were the row's sums and addresses, so a thread takes 16 where rows are long. Now that backward
-// takes 400 us (3.7 TB/s, 57 % of the measured copy rate: its 5 block-wide sums per row and 90 registers of
-// state leave two CTAs of 8 warps per SM to hide them), the forward of 32768 rows of 4096 in bf16 228 us (90 %).
+// takes 400 us (3.7 TB/s, 57 % of the measured copy rate: 1300 instructions per warp and row at 40 % of the
+// issue slots, the row's three sums and the copies' shared memory the rest, with two CTAs of 8 warps on an SM,
+// as the registers allow), the forward of 32768 rows of 4096 in bf16 228 us (90 %).
 // All sums are fp32 and taken in a fixed order.
 #include <algorithm>
 #include <type_traits>
@@ -209,12 +210,19 @@ constexpr int kRed = 64;     // floats of row_sum's shared memory: 16 + 32 + 16;
 constexpr int kInputs = 5;   // y, z, res, g_h, g_n
 
 // The row inputs: read from the thread's own copies in shared memory, which hold STAGES rows (one at work,
-// the others on their way), or, with STAGES = 0, from global memory.
+// the others on their way), or, with STAGES = 0, from global memory. STAGES = 1 (backward) is where two
+// whole rows do not fit: y and z, which a row needs to its end, have two places, and res, g_h and g_n, which
+// it has done with in its middle, one each, filled for the next row from there on (2048 rows of 16384 in bf16:
+// 406 us from global memory, 316 so; 8192 of 4096 in fp32: 321 us with one place of each, 306 so).
+// Neighbouring threads' pieces lie side by side: with a thread's pieces together, at an odd pitch, the copies
+// took as long again (forward 223 -> 355 us).
 template <typename IO, typename RES, int NV, int STAGES>
 struct RowInputs {
   const void* src[kInputs];
   uint32_t at[kInputs];  // of the tensor's part of a stage, this thread's first 16 bytes
-  uint32_t stage, bytes;
+  uint32_t stage, bytes;  // the row at work's place, and the distance between two
+  static constexpr bool kSplit = STAGES == 1;
+  static constexpr int kPlaces = kSplit ? 2 : STAGES, kTwice = 2;  // inputs before kTwice have two places
   int nvec, tid, tpr, width;
   int64_t row;
 
@@ -228,17 +236,19 @@ struct RowInputs {
     for (int k = 0; k < kInputs; ++k) {
       at[k] = smem + off + tid * 16;
       if (src[k]) off += NV * tpr * 16 * kParts(k);
+      if (kSplit && k == kTwice - 1) bytes = off, off *= 2;
     }
     stage = 0;
-    bytes = off;
+    if (!kSplit) bytes = off;
   }
-  // Starts this thread's copies of row r into a stage (an empty group behind the last row). `ahead` is the
-  // row's distance in channels from the tensors' beginnings.
+  // Starts this thread's copies of inputs FROM to TO - 1 of row r into a place (an empty group behind the
+  // last row). `ahead` is the row's distance in channels from the tensors' beginnings.
+  template <int FROM = 0, int TO = kSplit ? kTwice : kInputs>
   __device__ __forceinline__ void fetch(int64_t r, int64_t rows, int64_t ahead, uint32_t st) {
     if constexpr (STAGES == 0) return;
     if (r < rows) {
 #pragma unroll
-      for (int k = 0; k < kInputs; ++k) {
+      for (int k = FROM; k < TO; ++k) {
         if (!src[k]) continue;
         const uint8_t* from = reinterpret_cast<const uint8_t*>(src[k]) + ahead * (kParts(k) * 2);
 #pragma unroll
@@ -256,7 +266,14 @@ struct RowInputs {
   __device__ __forceinline__ void use(int64_t r, uint32_t st) {
     row = r;
     stage = st * bytes;
-    if constexpr (STAGES > 0) sm100::cp_async_wait<STAGES - 1>();
+    if constexpr (STAGES > 0) sm100::cp_async_wait<kSplit ? 2 : STAGES - 1>();
+  }
+  // kSplit's groups are y and z of a row, then the rest of it, then y and z of the next.
+  __device__ __forceinline__ void fetch_rest(int64_t r, int64_t rows, int64_t ahead) {
+    if constexpr (kSplit) fetch<kTwice, kInputs>(r, rows, ahead, 0);
+  }
+  __device__ __forceinline__ void use_rest() {
+    if constexpr (kSplit) sm100::cp_async_wait<1>();
   }
   template <int K>
   __device__ __forceinline__ void get(int i, float (&v)[8]) const {
@@ -268,7 +285,7 @@ struct RowInputs {
         uint4 q;
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
-                     : "r"(at[K] + stage + (h * NV + i) * tpr * 16));
+                     : "r"(at[K] + (kSplit && K >= kTwice ? 0 : stage) + (h * NV + i) * tpr * 16));
         return q;
       };
       if constexpr (sizeof(T) == 2) {
@@ -416,11 +433,13 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(con
   float* red = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(smem) + t.slot * slot_bytes);
   float* gred = red + 2 * kRed;
   const bool group_smem = norm_groups_in_smem(nvec, p.groups);
-  RowInputs<IO, RES, NV, STAGES> in(p, sm100::smem_u32(red + norm_sum_floats(nvec, p.groups)), tid, tpr);
+  using In = RowInputs<IO, RES, NV, STAGES>;
+  In in(p, sm100::smem_u32(red + norm_sum_floats(nvec, p.groups)), tid, tpr);
   const int64_t first = (int64_t)blockIdx.x * t.per_cta + t.slot, step = (int64_t)gridDim.x * t.per_cta;
   const float inv = 1.f / (float)p.width, ginv = (float)p.groups / (float)p.width;
 #pragma unroll
-  for (int k = 0; k < STAGES - 1; ++k) in.fetch(first + k * step, p.rows, (first + k * step) * p.width, k);
+  for (int k = 0; k < In::kPlaces - 1; ++k) in.fetch(first + k * step, p.rows, (first + k * step) * p.width, k);
+  in.fetch_rest(first, p.rows, first * p.width);
   F2 wp[NV][4], wn[NV][4], dwp[NV][4], dwn[NV][4];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -438,12 +457,11 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(con
   const bool gate_first = p.z && !p.gate_last, gate_last = p.z && p.gate_last;
   uint32_t st = 0;
   int red_row = 0;
-  int64_t ahead = (first + (STAGES - 1) * step) * p.width;
+  int64_t ahead = (first + (In::kPlaces - 1) * step) * p.width;
   for (int64_t row = first; row < p.rows; row += step) {
-    in.fetch(row + (STAGES - 1) * step, p.rows, ahead, st == 0 ? STAGES - 1 : st - 1);
-    ahead += step * p.width;
+    in.fetch(row + (In::kPlaces - 1) * step, p.rows, ahead, st == 0 ? In::kPlaces - 1 : st - 1);
     in.use(row, st);
-    if (++st == STAGES) st = 0;
+    if (++st == In::kPlaces) st = 0;
     const int64_t base = row * p.width;
     // the forward: a, its norm, h
     F2 hat[NV][4], h[NV][4];
@@ -475,6 +493,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(con
         for (int e = 0; e < 4; ++e) hat[i][e] = hat[i][e] * f2(r[i]);
       }
     }
+    in.use_rest();
     float s[2] = {0.f, 0.f};
     if (p.g_n) {
 #pragma unroll
@@ -546,6 +565,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(con
       }
       q[i] = f2_split(qq).x + f2_split(qq).y;
     }
+    in.fetch_rest(row + step, p.rows, ahead);
+    ahead += step * p.width;
     // the norm after the mixer and the gate before it
     if (p.w_post) group_sum<WARP, NV>(q, nvec, p.groups, tid, tpr, red + red_row + 48, gred);
     if (p.y) {
@@ -657,15 +678,17 @@ NormPlan norm_plan(const swimba_norm_dims* d, bool bwd) {
   n.threads = n.warp ? 128 : tpr;
   n.per_cta = n.warp ? 4 : 1;
   // as many rows in shared memory, up to three, as fit (as if every input were given) where a CTA has
-  // up to 256 threads beside another one (113 KB each), else alone (226 KB)
+  // up to 256 threads beside another one (113 KB each), else alone (226 KB); where only one does, the
+  // backward keeps y and z of two and the rest of one
   const size_t io = d->io_dtype == SWIMBA_BF16 ? 2 : 4, res = d->res_dtype == SWIMBA_BF16 ? 2 : 4;
   const size_t sums = (size_t)norm_sum_floats(nvec, d->groups) * 4;
   const size_t stage = (size_t)n.nv * tpr * 8 * (bwd ? 3 * io + 2 * res : 2 * io + res);
   const size_t pair = 113 * 1024, alone = 226 * 1024;
   auto fits = [&](int st, size_t room) { return (sums + st * stage) * n.per_cta <= room; };
+  const size_t split = (size_t)n.nv * tpr * 8 * (5 * io + 2 * res);
   if (n.threads <= 256) n.stages = fits(3, pair) ? 3 : fits(2, pair) ? 2 : 1;
-  else n.stages = fits(2, alone) ? 2 : 0;
-  n.slot_bytes = (int)(sums + n.stages * stage);
+  else n.stages = fits(2, alone) ? 2 : bwd && sums + split <= alone ? 1 : 0;
+  n.slot_bytes = (int)(sums + (n.stages == 1 ? split : n.stages * stage));
   const int fit = (int)std::min<size_t>(alone / ((size_t)n.slot_bytes * n.per_cta), 16);
   // (the backward's registers allow 512 threads of two vectors, 768 of one); no more CTAs than share the
   // rows evenly, since each writes its partial weight gradients
@@ -679,8 +702,9 @@ template <typename IO, typename RES, int NV, bool WARP, int STAGES, int MAXT>
 cudaError_t launch_norm(const NormPlan& n, const NormParams& p, bool bwd, cudaStream_t s) {
   const int smem = n.slot_bytes * n.per_cta;
   if (n.stages != STAGES || n.nv != NV || n.threads > MAXT) return cudaErrorInvalidConfiguration;
-  auto kernel = bwd ? norm_bwd_kernel<IO, RES, NV, WARP, STAGES, MAXT>
-                    : norm_fwd_kernel<IO, RES, NV, WARP, STAGES, MAXT>;
+  auto kernel = norm_bwd_kernel<IO, RES, NV, WARP, STAGES, MAXT>;
+  if constexpr (STAGES != 1) kernel = bwd ? kernel : norm_fwd_kernel<IO, RES, NV, WARP, STAGES, MAXT>;
+  else if (!bwd) return cudaErrorInvalidConfiguration;
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -693,7 +717,7 @@ cudaError_t launch_norm(const NormPlan& n, const NormParams& p, bool bwd, cudaSt
 template <typename IO, typename RES>
 cudaError_t run_norm(const swimba_norm_dims* d, const NormParams& p, bool bwd, cudaStream_t s) {
   const NormPlan n = norm_plan(d, bwd);
-  // (up to 256 channels three rows always fit, up to 2048 two, up to 4096 one)
+  // (up to 256 channels three rows always fit, up to 2048 two, up to 4096 two of the forward's)
   if (n.warp) return launch_norm<IO, RES, 1, true, 3, 128>(n, p, bwd, s);
   if (n.nv == 1)
     return n.stages == 3 ? launch_norm<IO, RES, 1, false, 3, 256>(n, p, bwd, s)
@@ -703,10 +727,12 @@ cudaError_t run_norm(const swimba_norm_dims* d, const NormParams& p, bool bwd, c
            : n.stages == 2 ? launch_norm<IO, RES, 2, false, 2, 256>(n, p, bwd, s)
                            : launch_norm<IO, RES, 2, false, 1, 256>(n, p, bwd, s);
   if (n.nv == 2)
-    return n.stages == 2 ? launch_norm<IO, RES, 2, false, 2, 512>(n, p, bwd, s)
-                         : launch_norm<IO, RES, 2, false, 0, 512>(n, p, bwd, s);
-  return n.stages == 2 ? launch_norm<IO, RES, 4, false, 2, 512>(n, p, bwd, s)
-                       : launch_norm<IO, RES, 4, false, 0, 512>(n, p, bwd, s);
+    return n.stages == 2   ? launch_norm<IO, RES, 2, false, 2, 512>(n, p, bwd, s)
+           : n.stages == 1 ? launch_norm<IO, RES, 2, false, 1, 512>(n, p, bwd, s)
+                           : launch_norm<IO, RES, 2, false, 0, 512>(n, p, bwd, s);
+  return n.stages == 2   ? launch_norm<IO, RES, 4, false, 2, 512>(n, p, bwd, s)
+         : n.stages == 1 ? launch_norm<IO, RES, 4, false, 1, 512>(n, p, bwd, s)
+                         : launch_norm<IO, RES, 4, false, 0, 512>(n, p, bwd, s);
 }
 
 cudaError_t run_norm_types(const swimba_norm_dims* d, const NormParams& p, bool bwd, cudaStream_t s) {
