@@ -103,6 +103,15 @@ def test_sizes(S, rows, width, groups, io, res_t):
 
 
 @pytest.mark.parametrize("gate_last", [False, True])
+@pytest.mark.parametrize("rows,width,groups,io,res_t", [
+    (900, 4096, 1, "bf16", "f32"), (900, 4096, 16, "f32", "f32"), (900, 4080, 5, "f32", "f32"), (460, 8192, 2, "bf16", "f32"),
+    (460, 16384, 1, "bf16", "bf16"), (460, 12288, 3, "f32", "bf16")])
+def test_wide_rows_one_after_the_other(S, rows, width, groups, io, res_t, gate_last):
+    """Several rows per CTA where shared memory holds one, one and a half, or two."""
+    Case(10, rows, width, groups, io, res_t, gate_last=gate_last).check(S)
+
+
+@pytest.mark.parametrize("gate_last", [False, True])
 @pytest.mark.parametrize("parts", ["z", "post", "res", "pre", "z post", "z res", "post pre", "z pre", "post res", "res pre",
                                    "z post res", "z post pre", "z res pre", "post res pre", "z post res pre", ""])
 def test_parts(S, parts, gate_last):
