@@ -211,27 +211,48 @@ __global__ void __launch_bounds__(128) la_chain_kernel(const __grid_constant__ L
 // ---- rows without a token, shared heads ----------------------------------------------------------------
 // out[b, t, kv, :] = Σ_i part[b, t, kv group + i, :] for tokens inside the sequence (fixed order), zeros
 // in the rows behind it; with part == null only the zeros are written. One thread per 8 elements.
+struct LaRowsOf {
+  void* out;
+  int64_t st;         // elements from one token to the next
+  const float* part;  // [rows, heads, group, d], or null: only zeros behind the sequences' ends
+  int heads, d;
+};
+struct LaRows {
+  LaRowsOf of[3];
+  const int32_t* lens;  // or null
+  int64_t B, L;
+  int group;
+};
 template <typename IO>
-__global__ void __launch_bounds__(256) la_rows_kernel(IO* out, int64_t st, int64_t sb, const float* part, int group,
-                                                      int width, int d, int64_t L, const int32_t* lens, int64_t total) {
+__global__ void __launch_bounds__(256) la_rows_kernel(const __grid_constant__ LaRows p) {
+  const LaRowsOf& r = p.of[blockIdx.y];
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= total) return;
-  const int per = width / 8;
-  const int64_t row = i / per, b = row / L, t = row - b * L;
+  const int width = r.heads * r.d, per = width / 8;
+  const int64_t row = i / per, b = row / p.L, t = row - b * p.L;
+  if (b >= p.B) return;
   const int at = (int)(i - row * per) * 8;
-  const bool live = lens == nullptr || t < (int64_t)lens[b];
-  if (live && part == nullptr) return;
+  const bool live = p.lens == nullptr || t < (int64_t)p.lens[b];
+  if (live && r.part == nullptr) return;
   float v[8] = {};
   if (live) {
-    const int kv = at / d, j = at - kv * d;
-    const float* src = part + (row * (width / d) * group + (int64_t)kv * group) * d + j;
-    for (int g = 0; g < group; ++g)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += src[(int64_t)g * d + e];
+    const int kv = at / r.d, j = at - kv * r.d;
+    const float* src = r.part + (row * width + (int64_t)kv * r.d) * p.group + j;
+    for (int g = 0; g < p.group; ++g) {
+      const float4 a = *reinterpret_cast<const float4*>(src + g * r.d), c = *reinterpret_cast<const float4*>(src + g * r.d + 4);
+      v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+      v[4] += c.x, v[5] += c.y, v[6] += c.z, v[7] += c.w;
+    }
   }
-  IO* dst = out + b * sb + t * st + at;
+  IO* dst = reinterpret_cast<IO*>(r.out) + row * r.st + at;
+  if constexpr (sizeof(IO) == 2) {
+    __align__(16) IO x[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) from_f32(dst[e], v[e]);
+    for (int e = 0; e < 8; ++e) from_f32(x[e], v[e]);
+    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(x);
+  } else {
+    reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
 }
 
 // ---- decode step ----------------------------------------------------------------------------------------
@@ -428,12 +449,12 @@ cudaError_t run_tc(const LaParams& p, cudaStream_t s) {
 
 cudaError_t run_roles(const LaParams& p, bool bf16, cudaStream_t s) { return bf16 ? run_tc(p, s) : run_simt(p, s); }
 
-template <typename IO>
-void launch_rows(void* out, int64_t st, const float* part, int group, int kv, int d, const swimba_linattn_dims* dims,
-                 const int32_t* lens, cudaStream_t s) {
-  const int64_t total = dims->batch * dims->seqlen * kv * d / 8;
-  la_rows_kernel<IO><<<(unsigned)((total + 255) / 256), 256, 0, s>>>(static_cast<IO*>(out), st, st * dims->seqlen, part,
-                                                                    group, kv * d, d, dims->seqlen, lens, total);
+// One launch over n gradients, whose widest has `width` channels.
+void launch_rows(const LaRows& p, int n, int width, bool bf16, cudaStream_t s) {
+  if (n == 0) return;
+  const dim3 grid((unsigned)((p.B * p.L * (width / 8) + 255) / 256), (unsigned)n);
+  if (bf16) la_rows_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
+  else la_rows_kernel<float><<<grid, 256, 0, s>>>(p);
   note_launch();
 }
 
@@ -590,14 +611,21 @@ swimba_status swimba_linattn_bwd(const swimba_linattn_dims* dims, const void* q,
   const bool bf16 = dims->io_dtype == SWIMBA_BF16;
   const cudaError_t e = run_roles(p, bf16, s);
   if (e != cudaSuccess) return api_cuda_status(e);
-  auto rows = [&](void* dst, int64_t stride, const float* part, int heads, int d) {
+  LaRows rows{};
+  rows.lens = lens;
+  rows.B = dims->batch;
+  rows.L = L;
+  rows.group = group;
+  int n = 0, width = 0;
+  auto add = [&](void* dst, int64_t stride, const float* part, int heads, int d) {
     if (part == nullptr && lens == nullptr) return;
-    if (bf16) launch_rows<__nv_bfloat16>(dst, stride, part, group, heads, d, dims, lens, s);
-    else launch_rows<float>(dst, stride, part, group, heads, d, dims, lens, s);
+    rows.of[n++] = LaRowsOf{dst, stride, part, heads, d};
+    width = std::max(width, heads * d);
   };
-  rows(dq, dims->q_stride, nullptr, H, d_k);
-  rows(dk, dims->k_stride, shared ? at(ws, l.part_k) : nullptr, dims->n_kv_heads, d_k);
-  rows(dv, dims->v_stride, shared ? at(ws, l.part_v) : nullptr, dims->n_kv_heads, d_v);
+  add(dq, dims->q_stride, nullptr, H, d_k);
+  add(dk, dims->k_stride, shared ? at(ws, l.part_k) : nullptr, dims->n_kv_heads, d_k);
+  add(dv, dims->v_stride, shared ? at(ws, l.part_v) : nullptr, dims->n_kv_heads, d_v);
+  launch_rows(rows, n, width, bf16, s);
   return api_cuda_status(cudaGetLastError());
 }
 
