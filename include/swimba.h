@@ -446,8 +446,8 @@ swimba_status swimba_block_step(const swimba_block_dims *bd, const void *u,
  * bf16: chunks of 128 tokens on the tensor cores; the masked, decayed scores and the state's copy
  * for the readout are rounded to bf16 once each, everything that is carried on stays fp32 (values
  * enter the state update as two or three bf16 parts: 24 bits where S_final or dS0 is asked for and the
- * decay to it is above 2^-6, else 16). fp32: the recurrence in
- * fp32 on the SIMT cores. A value that is not finite may spread to every output of its chunk of 128
+ * decay to it is above 2^-6, else 16). fp32, and bf16 of at most 8 tokens: the recurrence in fp32 on
+ * the SIMT cores. A value that is not finite may spread to every output of its chunk of 128
  * tokens and to what follows it in its sequence (for the gradients of keys and values: to what
  * precedes it), never to another sequence. Outputs overlap nothing but what is said below. */
 typedef struct {

@@ -368,7 +368,12 @@ struct LaLayout {
   size_t seg[kLaMaxRoles], part_k, part_v, flags, states, total;
 };
 
-bool la_use_tc(const swimba_linattn_dims* d) { return d->io_dtype == SWIMBA_BF16; }
+// bf16 sequences of a few tokens take the recurrence too: a chunk costs the same however few it holds, and nothing
+// but the output is rounded. Chunk against recurrence, 64 sequences x 32 heads of 128 forward, 128 x 32 backward:
+// 4 tokens 134 against 96 us and 510 against 264, 8 tokens 134 / 115 and 510 / 402, 16 tokens 134 / 161 and 510 / 684.
+constexpr int kLaShort = 8;
+static_assert(kLaShort <= kLaSimtChunk, "bf16 sequences on the SIMT cores have one segment");
+bool la_use_tc(const swimba_linattn_dims* d) { return d->io_dtype == SWIMBA_BF16 && d->seqlen > kLaShort; }
 
 LaLayout la_layout(const swimba_linattn_dims* d, const LaPlan& pl, int roles) {
   LaLayout l{};
@@ -398,28 +403,30 @@ void launch_chain(const LaParams& p, cudaStream_t s) {
   note_launch();
 }
 
-template <int NI>
+template <typename IO, int NI>
 cudaError_t launch_simt(const LaParams& p, int max_dw, cudaStream_t s) {
   const dim3 grid((unsigned)((int64_t)p.n_roles * p.B * p.H * p.nseg), (unsigned)((max_dw + kSimtCols - 1) / kSimtCols));
   if (p.nseg > 1) {
-    la_simt_kernel<float, NI, 1><<<grid, 128, 0, s>>>(p);
+    if constexpr (sizeof(IO) == 4) la_simt_kernel<IO, NI, 1><<<grid, 128, 0, s>>>(p);
+    else return cudaErrorInvalidConfiguration;  // see kLaShort
     note_launch();
     launch_chain(p, s);
   }
-  la_simt_kernel<float, NI, 0><<<grid, 128, 0, s>>>(p);
+  la_simt_kernel<IO, NI, 0><<<grid, 128, 0, s>>>(p);
   note_launch();
   return cudaGetLastError();
 }
 
+template <typename IO>
 cudaError_t run_simt(const LaParams& p, cudaStream_t s) {
   int dx = 0, dw = 0;
   for (int i = 0; i < p.n_roles; ++i) {
     dx = std::max(dx, p.role[i].dx);
     dw = std::max(dw, p.role[i].dw);
   }
-  if (dx <= 32) return launch_simt<2>(p, dw, s);
-  if (dx <= 64) return launch_simt<4>(p, dw, s);
-  return dx <= 96 ? launch_simt<6>(p, dw, s) : launch_simt<8>(p, dw, s);
+  if (dx <= 32) return launch_simt<IO, 2>(p, dw, s);
+  if (dx <= 64) return launch_simt<IO, 4>(p, dw, s);
+  return dx <= 96 ? launch_simt<IO, 6>(p, dw, s) : launch_simt<IO, 8>(p, dw, s);
 }
 
 // The tensor-core kernel takes roles of one padded size (64 or 128) together: all three where d_k and
@@ -447,7 +454,9 @@ cudaError_t run_tc(const LaParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t run_roles(const LaParams& p, bool bf16, cudaStream_t s) { return bf16 ? run_tc(p, s) : run_simt(p, s); }
+cudaError_t run_roles(const LaParams& p, bool tc, bool bf16, cudaStream_t s) {
+  return tc ? run_tc(p, s) : bf16 ? run_simt<__nv_bfloat16>(p, s) : run_simt<float>(p, s);
+}
 
 // One launch over n gradients, whose widest has `width` channels.
 void launch_rows(const LaRows& p, int n, int width, bool bf16, cudaStream_t s) {
@@ -525,7 +534,7 @@ swimba_status swimba_linattn_fwd(const swimba_linattn_dims* dims, const void* q,
   r.sc = 1;
   r.seg = pl.nseg > 1 ? at(ws, l.seg[0]) : nullptr;
   r.parts = S_final != nullptr ? 3 : 2;
-  return api_cuda_status(run_roles(p, dims->io_dtype == SWIMBA_BF16, static_cast<cudaStream_t>(stream)));
+  return api_cuda_status(run_roles(p, pl.tc, dims->io_dtype == SWIMBA_BF16, static_cast<cudaStream_t>(stream)));
 }
 
 swimba_status swimba_linattn_step(const swimba_linattn_dims* dims, const void* q, const void* k, const void* v,
@@ -609,7 +618,7 @@ swimba_status swimba_linattn_bwd(const swimba_linattn_dims* dims, const void* q,
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf16 = dims->io_dtype == SWIMBA_BF16;
-  const cudaError_t e = run_roles(p, bf16, s);
+  const cudaError_t e = run_roles(p, pl.tc, bf16, s);
   if (e != cudaSuccess) return api_cuda_status(e);
   LaRows rows{};
   rows.lens = lens;

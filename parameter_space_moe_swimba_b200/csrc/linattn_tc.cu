@@ -1,5 +1,5 @@
 // Linear attention with a decay for each head, in chunks of 128 tokens on the tcgen05 tensor cores
-// (bf16 tensors; the roles are those of linattn.cuh, in forward order here).
+// (bf16 tensors of more than a few tokens; the roles are those of linattn.cuh, in forward order here).
 //
 // For a chunk of n <= 128 tokens and the state M [dx, dw] before it, with γ = exp(log_decay):
 //   P[i, s]  = γ^(i-s) (x_i · y_s) for s <= i, else 0          A = X, B = Y        (K = dx)

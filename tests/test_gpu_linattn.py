@@ -122,6 +122,10 @@ CASES = {
     "split_lens": dict(B=2, L=1700, H=2, KV=1, dk=32, dv=64, lens=[1430, 400]),
     # more heads than SMs, not a multiple: sequences are cut between two CTAs
     "cut": dict(B=1, L=900, H=149, KV=149, dk=16, dv=24),
+    # the longest sequences that bf16 takes token by token, and the shortest that it does not
+    "short": dict(B=3, L=8, H=6, KV=2, dk=64, dv=128, fused=True),
+    "short_lens": dict(B=4, L=7, H=4, KV=1, dk=128, dv=72, lens=[7, 0, 3, 9]),
+    "chunk_of_9": dict(B=3, L=9, H=6, KV=2, dk=64, dv=128, fused=True),
     "no_start": dict(B=2, L=200, H=2, KV=2, dk=128, dv=128, start=False),
     "split_no_start": dict(B=1, L=1500, H=1, KV=1, dk=128, dv=128, start=False),
 }
@@ -156,6 +160,21 @@ def test_backward(S, name, dtype):
     for got, r, what in ((dk, rk, "dk"), (dv, rv, "dv")):
         c.close(got, *(M.sum_shared(x, KV) for x in (r.out, r.once, r.mag)), what)
     c.close(dS0, rv.M, None, rv.M_mag, "dS0", out=False)
+
+
+@pytest.mark.parametrize("L", [1, 3, 8])
+def test_a_few_bf16_tokens_are_rounded_at_the_end_only(S, L):
+    c = Case(11, 2, L, 4, 4, 128, 64, "bf16")
+    a = c.np
+    o, S_final = c.forward(S)
+    r = M.linattn_forward(a["q"], a["k"], a["v"], a["g"], c.scale, None, a["S0"])
+    c.close(Case.f64(o), r.out, 0, r.mag, "o")
+    c.close(Case.f64(S_final), r.M, None, r.M_mag, "S_final", out=False)
+    got = [Case.f64(x) for x in c.backward(S)]
+    roles = M.linattn_backward(a["q"], a["k"], a["v"], a["g"], c.scale, a["g_o"], None, a["S0"], a["g_S"])
+    for x, r, what in zip(got, roles, ("dq", "dk", "dv")):
+        c.close(x, r.out, 0, r.mag, what)
+    c.close(got[3], roles[2].M, None, roles[2].M_mag, "dS0", out=False)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
