@@ -19,7 +19,7 @@
 // registers. Without the copies a row's loads waited for the row before it (16384 rows of 4096, bf16
 // with an fp32 residual, backward: 547 us, 2.7 TB/s); with 8 channels per thread a third of the
 // instructions were the row's sums and addresses, so a thread takes 16 where rows are long. Now that backward
-// takes 400 us (3.7 TB/s, 57 % of the measured copy rate: 1300 instructions per warp and row at 40 % of the
+// takes 389 us (3.8 TB/s, 58 % of the measured copy rate: 1300 instructions per warp and row at 40 % of the
 // issue slots, the row's three sums and the copies' shared memory the rest, with two CTAs of 8 warps on an SM,
 // as the registers allow), the forward of 32768 rows of 4096 in bf16 228 us (90 %).
 // All sums are fp32 and taken in a fixed order.
@@ -75,7 +75,7 @@ __device__ __forceinline__ void store8(void* base, int64_t at, const float (&v)[
 }
 
 // Two floats in one 64-bit register pair: the packed fp32 instructions round each as the scalar ones do and
-// take half the issue slots, which bound the backward (439 -> 391 us; the forward, which memory bounds, is
+// take half the issue slots, which bound the backward (439 -> 400 us; the forward, which memory bounds, is
 // faster with scalar ones: 240 against 267 us).
 struct F2 {
   unsigned long long v;
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(con
 #pragma unroll
   for (int k = 0; k < In::kPlaces - 1; ++k) in.fetch(first + k * step, p.rows, (first + k * step) * p.width, k);
   in.fetch_rest(first, p.rows, first * p.width);
-  F2 wp[NV][4], wn[NV][4], dwp[NV][4], dwn[NV][4];
+  F2 wp[NV][4], wn[NV][4], dwp[NV][4], dwn[NV][4];  // wp: β w_post; dwp without its β until the end
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = tid + i * tpr;
@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(con
     if (v < nvec && p.w_pre) load8<float>(p.w_pre, 8 * v, b);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      wp[i][e] = p.w_post ? f2(a[2 * e], a[2 * e + 1]) : f2(1.f);
+      wp[i][e] = p.w_post ? f2(p.beta * a[2 * e], p.beta * a[2 * e + 1]) : f2(p.beta);
       wn[i][e] = f2(b[2 * e], b[2 * e + 1]);
       dwp[i][e] = dwn[i][e] = f2(0.f);
     }
@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(con
         F2 s0 = f2(0.f), s1 = f2(0.f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          F2 q = hat[i][e] * (wp[i][e] * f2(p.beta));
+          F2 q = hat[i][e] * wp[i][e];
           if (gate_last) q = q * (z[e] * f2_sigmoid(z[e]));
           h[i][e] = f2_fma(f2(p.alpha), h[i][e], q);
           s0 = f2_fma(h[i][e], h[i][e], s0);
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(con
       }
       row_sum<WARP, 2>(s, red + red_row + 16);
     }
-    const float rh = p.g_n ? rsqrtf(fmaf(s[0], inv, p.eps)) : 0.f, m = s[1] * rh * inv;
+    const float rh = p.g_n ? rsqrtf(fmaf(s[0], inv, p.eps)) : 0.f, back = -(s[1] * rh * inv) * rh * rh;  // (rh³ alone would leave the range first)
     // back through the norm before the next block, the residual, the gate behind the norm
     float q[NV];
 #pragma unroll
@@ -532,9 +532,9 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(con
         in.template get<4>(i, gn);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const F2 hh = h[i][e] * f2(rh);
-          dwn[i][e] = f2_fma(gn[e], hh, dwn[i][e]);
-          dh[e] = f2_fma(f2(rh), f2_fma(hh, f2(-m), gn[e] * wn[i][e]), dh[e]);
+          const F2 g = gn[e] * f2(rh);
+          dwn[i][e] = f2_fma(g, h[i][e], dwn[i][e]);
+          dh[e] = f2_fma(h[i][e], f2(back), f2_fma(g, wn[i][e], dh[e]));
         }
       }
       if (p.dres) {
@@ -543,16 +543,14 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(con
         for (int e = 0; e < 4; ++e) d[e] = dh[e] * f2(p.alpha);
         store8<RES>(p.dres, base + 8 * v, d);
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) dh[e] = dh[e] * f2(p.beta);
       if (gate_last) {
         F2 z[4], dz[4];
         in.template get<1>(i, z);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const F2 sg = f2_sigmoid(z[e]);
-          dz[e] = dh[e] * (hat[i][e] * wp[i][e]) * (sg * f2_fma(z[e], f2_fma(sg, f2(-1.f), f2(1.f)), f2(1.f)));
-          dh[e] = dh[e] * (z[e] * sg);
+          const F2 sg = f2_sigmoid(z[e]), zs = z[e] * sg;
+          dz[e] = dh[e] * (hat[i][e] * wp[i][e]) * f2_fma(zs, f2_fma(sg, f2(-1.f), f2(1.f)), sg);
+          dh[e] = dh[e] * zs;
         }
         store8<IO>(p.dz, base + 8 * v, dz);
       }
@@ -585,9 +583,9 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(con
           in.template get<1>(i, z);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const F2 sg = f2_sigmoid(z[e]);
-            dz[e] = h[i][e] * y[e] * (sg * f2_fma(z[e], f2_fma(sg, f2(-1.f), f2(1.f)), f2(1.f)));
-            h[i][e] = h[i][e] * (z[e] * sg);
+            const F2 sg = f2_sigmoid(z[e]), zs = z[e] * sg;
+            dz[e] = h[i][e] * y[e] * f2_fma(zs, f2_fma(sg, f2(-1.f), f2(1.f)), sg);
+            h[i][e] = h[i][e] * zs;
           }
           store8<IO>(p.dz, base + 8 * v, dz);
         }
@@ -614,7 +612,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(con
           F2 o[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            o[e] = w ? dwn[i][e] : dwp[i][e];
+            o[e] = w ? dwn[i][e] : dwp[i][e] * f2(p.beta);
             if (k > 0) o[e] = o[e] + f2(d[2 * e], d[2 * e + 1]);
           }
           store8<float>(d, 0, o);

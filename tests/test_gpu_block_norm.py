@@ -136,6 +136,16 @@ def test_weight_gradients_over_rows(S, rows):
     Case(6, rows, 1536, 1, "bf16", "bf16").check(S)
 
 
+@pytest.mark.parametrize("size,eps", [(1e-12, 1e-28), (1e12, 1e-5), (0.0, 1e-30)])
+def test_sizes_of_values_far_from_one(S, size, eps):
+    """Rows of tiny, huge and no values: no intermediate leaves fp32's range where the results do not."""
+    c = Case(12, 20, 1024, io="f32", res_t="f32", z=False, post=False, eps=eps)
+    c.y *= size
+    c.res *= size
+    c.g_h *= min(1.0, 1 / max(size, 1e-12))
+    c.check(S)
+
+
 def test_rows_of_zeros_and_rows_that_are_not_finite(S):
     c = Case(7, 6, 256, 2, "bf16", "bf16", gate_last=True)
     clean = c.forward(S)
