@@ -3,12 +3,14 @@
 Every function named ``swimba_*`` here calls the C function of the same name with device pointers
 taken from torch tensors (``tensor.data_ptr()``) and the current torch CUDA stream unless one is
 given. Every step of the layer runs in the library's CUDA kernels; there is no Python or CPU
-compute path. Importing this module fails loudly when the library has not been built.
+compute path. The linear attention and block norm calls answer SWIMBA_ERR_INVALID_ARG where a tensor's
+type, size, layout or device is not what the call's dims say; a workspace counts for what it holds. Importing this module fails loudly when the library has not been built.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -268,27 +270,65 @@ def _same_places(t, st, lay, dims) -> bool:
             and (st[2] == lay[2] or t.shape[2] == 1) and (st[3] == 1 or t.shape[3] == 1))
 
 
-def _pointers(dense, dims=None, strided=()):
-    """Device pointers of a call's tensors: [B, L, heads, d] ones, each with the token stride that the call's
-    dims state for it, then those that have to be dense. None where one is laid out differently or lies on
-    another device than the current one, whose stream the call would use (a CPU tensor's is -1, no device yet
-    -2). Integers are taken as pointers and not looked at."""
+def _pointers(dense, dims=None, strided=(), Tensor=torch.Tensor):
+    """Device pointers of a call's tensors: [B, L, heads, d] ones, each with the token stride that the call's dims
+    state for it and its dtype, shape and strides (or only its channels per head), then those that have to be dense,
+    with their dtype and number of elements (or alone: a workspace). None where one has another type or size, is
+    laid out differently or lies on another device than the current one, whose stream the call would use (a CPU
+    tensor's is -1, no device yet -2): it would be read as other values, or read and written past its end.
+    Integers are taken as pointers and not looked at."""
     device = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
     out = []
-    for t, stride, d in strided:
-        if isinstance(t, torch.Tensor):
-            lay, st = (dims.seqlen * stride, stride, d, 1), t.stride()
+    for t, stride, of in strided:
+        if isinstance(t, Tensor):
+            if of.__class__ is tuple:
+                dtype, shape, lay = of
+                if t.dtype is not dtype or t.shape != shape:
+                    return None
+            else:
+                lay = (dims.seqlen * stride, stride, of, 1)
+            st = t.stride()
             if t.get_device() != device or (st != lay and not _same_places(t, st, lay, dims)):
                 return None
             t = t.data_ptr()
         out.append(t)
     for t in dense:
-        if isinstance(t, torch.Tensor):
+        if t.__class__ is tuple:
+            t, dtype, size = t
+            if isinstance(t, Tensor):
+                if t.dtype is not dtype or t.numel() != size or t.get_device() != device or not t.is_contiguous():
+                    return None
+                t = t.data_ptr()
+        elif isinstance(t, Tensor):
             if t.get_device() != device or not t.is_contiguous():
                 return None
             t = t.data_ptr()
         out.append(t)
     return out
+
+
+_F32, _IO_DTYPE = torch.float32, {SWIMBA_F32: torch.float32, SWIMBA_BF16: torch.bfloat16}
+_LINATTN_FIELDS, _NORM_FIELDS = struct.Struct("qqiiiiqqqif"), struct.Struct("qiiiiifff")  # all of them in 0.2 us
+
+
+def _linattn_sizes(dims):
+    """What a linear attention call's tensors have to be: the io dtype, heads, sequences, the token stride of q, k and v
+    with (dtype, shape, strides), the elements of o and of the states."""
+    B, L, H, KV, dk, dv, qs, ks, vs, io, _ = _LINATTN_FIELDS.unpack_from(dims)
+    io = _IO_DTYPE.get(io)
+    return (io, H, B, qs, (io, (B, L, H, dk), (L * qs, qs, dk, 1)), ks, (io, (B, L, KV, dk), (L * ks, ks, dk, 1)),
+            vs, (io, (B, L, KV, dv), (L * vs, vs, dv, 1)), B * L * H * dv, B * H * dk * dv)
+
+
+def _norm_sizes(dims):
+    """The io and residual dtypes of a block norm call, its width and its elements."""
+    rows, width, _, io, res, _, _, _, _ = _NORM_FIELDS.unpack_from(dims)
+    return _IO_DTYPE.get(io), _IO_DTYPE.get(res), width, rows * width
+
+
+def _room(ws, ws_bytes) -> int:
+    """The workspace bytes that a call may use: what the caller says, but no more than the tensor has."""
+    return min(int(ws_bytes), ws.nbytes) if isinstance(ws, torch.Tensor) else int(ws_bytes)
 
 
 def check(status: int, where: str = "swimba") -> None:
@@ -457,30 +497,36 @@ def swimba_linattn_workspace_size(dims: swimba_linattn_dims, op: int) -> int:
 
 
 def swimba_linattn_fwd(dims, q, k, v, log_decay, lens, S0, o, S_final, ws, ws_bytes, stream=None) -> int:
-    p = _pointers((log_decay, lens, S0, o, S_final, ws), dims,
-                  ((q, dims.q_stride, dims.d_k), (k, dims.k_stride, dims.d_k), (v, dims.v_stride, dims.d_v)))
-    return 1 if p is None else _lib.swimba_linattn_fwd(ctypes.byref(dims), *p, ws_bytes, _stream(stream))
+    io, H, B, qs, of_q, ks, of_k, vs, of_v, outs, states = _linattn_sizes(dims)
+    p = _pointers(((log_decay, _F32, H), (lens, torch.int32, B), (S0, _F32, states), (o, io, outs),
+                   (S_final, _F32, states), ws), dims, ((q, qs, of_q), (k, ks, of_k), (v, vs, of_v)))
+    return 1 if p is None else _lib.swimba_linattn_fwd(ctypes.byref(dims), *p, _room(ws, ws_bytes), _stream(stream))
 
 
 def swimba_linattn_step(dims, q, k, v, log_decay, S_in, o, S_out, stream=None) -> int:
-    p = _pointers((log_decay, S_in, o, S_out), dims,
-                  ((q, dims.q_stride, dims.d_k), (k, dims.k_stride, dims.d_k), (v, dims.v_stride, dims.d_v)))
+    io, H, _, qs, of_q, ks, of_k, vs, of_v, outs, states = _linattn_sizes(dims)
+    p = _pointers(((log_decay, _F32, H), (S_in, _F32, states), (o, io, outs), (S_out, _F32, states)), dims,
+                  ((q, qs, of_q), (k, ks, of_k), (v, vs, of_v)))
     return 1 if p is None else _lib.swimba_linattn_step(ctypes.byref(dims), *p, _stream(stream))
 
 
 def swimba_linattn_bwd(dims, q, k, v, log_decay, lens, S0, g_o, g_S, dq, dk, dv, dS0, ws, ws_bytes, stream=None) -> int:
-    ql, kl, vl = (dims.q_stride, dims.d_k), (dims.k_stride, dims.d_k), (dims.v_stride, dims.d_v)
-    p = _pointers((log_decay, lens, S0, g_o, g_S, dS0, ws), dims,
-                  ((q, *ql), (k, *kl), (v, *vl), (dq, *ql), (dk, *kl), (dv, *vl)))
+    io, H, B, qs, of_q, ks, of_k, vs, of_v, outs, states = _linattn_sizes(dims)
+    p = _pointers(((log_decay, _F32, H), (lens, torch.int32, B), (S0, _F32, states), (g_o, io, outs), (g_S, _F32, states),
+                   (dS0, _F32, states), ws), dims,
+                  ((q, qs, of_q), (k, ks, of_k), (v, vs, of_v), (dq, qs, of_q), (dk, ks, of_k), (dv, vs, of_v)))
     if p is None:
         return 1
+    room = _room(ws, ws_bytes)
     q, k, v, dq, dk, dv, log_decay, lens, S0, g_o, g_S, dS0, ws = p
     return _lib.swimba_linattn_bwd(ctypes.byref(dims), q, k, v, log_decay, lens, S0, g_o, g_S, dq, dk, dv, dS0, ws,
-                                   ws_bytes, _stream(stream))
+                                   room, _stream(stream))
 
 
 def swimba_block_norm_fwd(dims, y, z, w_post, res, w_pre, h, n, stream=None) -> int:
-    p = _pointers((y, z, w_post, res, w_pre, h, n))
+    io, rt, width, size = _norm_sizes(dims)
+    p = _pointers(((y, io, size), (z, io, size), (w_post, _F32, width), (res, rt, size), (w_pre, _F32, width),
+                   (h, rt, size), (n, io, size)))
     return 1 if p is None else _lib.swimba_block_norm_fwd(ctypes.byref(dims), *p, _stream(stream))
 
 
@@ -490,8 +536,11 @@ def swimba_block_norm_workspace_size(dims: swimba_norm_dims) -> int:
 
 def swimba_block_norm_bwd(dims, y, z, w_post, res, w_pre, g_h, g_n, dy, dz, dres, dw_post, dw_pre, ws, ws_bytes,
                           stream=None) -> int:
-    p = _pointers((y, z, w_post, res, w_pre, g_h, g_n, dy, dz, dres, dw_post, dw_pre, ws))
-    return 1 if p is None else _lib.swimba_block_norm_bwd(ctypes.byref(dims), *p, ws_bytes, _stream(stream))
+    io, rt, width, size = _norm_sizes(dims)
+    p = _pointers(((y, io, size), (z, io, size), (w_post, _F32, width), (res, rt, size), (w_pre, _F32, width),
+                   (g_h, rt, size), (g_n, io, size), (dy, io, size), (dz, io, size), (dres, rt, size),
+                   (dw_post, _F32, width), (dw_pre, _F32, width), ws))
+    return 1 if p is None else _lib.swimba_block_norm_bwd(ctypes.byref(dims), *p, _room(ws, ws_bytes), _stream(stream))
 
 
 # ------------------------------------------------------------------------------------------------
@@ -519,7 +568,11 @@ def make_dims(cfg, seqlen=None, batch=None, n_experts=None, top_k=None) -> swimb
     )
 
 
-_TORCH_DTYPE = {torch.float32: SWIMBA_F32, torch.bfloat16: SWIMBA_BF16}
+def _io_code(t: torch.Tensor) -> int:
+    for code, dtype in _IO_DTYPE.items():
+        if t.dtype is dtype:
+            return code
+    raise SwimbaError(1, f"tensor of {t.dtype}, not float32 or bfloat16")
 
 
 def _token_stride(t: torch.Tensor) -> int:
@@ -536,12 +589,14 @@ def _token_stride(t: torch.Tensor) -> int:
 def make_linattn_dims(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: float) -> swimba_linattn_dims:
     """Dims of q [B, L, H, d_k], k [B, L, Hkv, d_k], v [B, L, Hkv, d_v] as they lie in memory: dense, or
     columns of one projection's output."""
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise SwimbaError(1, f"linear attention of q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
     B, L, H, dk = q.shape
     if k.shape[:2] != (B, L) or k.shape[3] != dk or v.shape[:3] != k.shape[:3] or len({q.dtype, k.dtype, v.dtype}) > 1:
         raise SwimbaError(1, f"linear attention of q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
     return swimba_linattn_dims(batch=B, seqlen=L, n_heads=H, n_kv_heads=k.shape[2], d_k=dk, d_v=v.shape[3],
                                q_stride=_token_stride(q), k_stride=_token_stride(k), v_stride=_token_stride(v),
-                               io_dtype=_TORCH_DTYPE[q.dtype], scale=float(scale))
+                               io_dtype=_io_code(q), scale=float(scale))
 
 
 def new_linattn_workspace(dims: swimba_linattn_dims, op: int, device="cuda") -> torch.Tensor:
@@ -558,8 +613,8 @@ def make_norm_dims(y: torch.Tensor, h: torch.Tensor, groups: int = 1, eps: float
     if y.shape != h.shape:
         raise SwimbaError(1, f"block norm of y {tuple(y.shape)} and h {tuple(h.shape)}")
     width = y.shape[-1]
-    return swimba_norm_dims(rows=y.numel() // max(1, width), width=width, groups=groups, io_dtype=_TORCH_DTYPE[y.dtype],
-                            res_dtype=_TORCH_DTYPE[h.dtype], gate_last=int(gate_last), eps=eps, res_scale=res_scale,
+    return swimba_norm_dims(rows=y.numel() // max(1, width), width=width, groups=groups, io_dtype=_io_code(y),
+                            res_dtype=_io_code(h), gate_last=int(gate_last), eps=eps, res_scale=res_scale,
                             out_scale=out_scale)
 
 

@@ -200,3 +200,94 @@ def test_norm_arguments(S):
     assert norm_bwd(S, d, ws=FAKE + 8) == ALIGN
     with pytest.raises(S.SwimbaError):
         S.make_norm_dims(torch.zeros(3, 8), torch.zeros(4, 8))
+
+
+class Called:
+    """Stands in for the library: a call that got past the binding's checks."""
+
+    def __init__(self):
+        self.args = None
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.args = args
+            return 0
+
+        return call
+
+
+@pytest.fixture
+def taken(S, monkeypatch):
+    """Runs a binding call on CPU tensors that stand in for the device's (named -1), without the library."""
+    monkeypatch.setattr(S.torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(S.torch.cuda, "current_device", lambda: -1)
+    lib = Called()
+    monkeypatch.setattr(S, "_lib", lib)
+    return lib
+
+
+# Of each tensor: another type, a smaller batch or fewer tokens, more of them.
+def _others(x):
+    other = {torch.float32: torch.bfloat16, torch.bfloat16: torch.float16, torch.int32: torch.int64}[x.dtype]
+    return x.to(other), x[1:], x[:, :-1] if x.dim() > 1 else x[:-1], torch.cat((x, x))
+
+
+@pytest.mark.parametrize("t", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B", [1, 2])
+def test_linattn_tensors_have_the_dims_types_and_sizes(S, taken, t, B):
+    """lens as int64, a state in the io type, an output of a smaller batch, gradients of fewer tokens: refused."""
+    L, H, KV, dk, dv = 5, 4, 2, 16, 24
+    new = lambda *s, t=t: torch.zeros(s, dtype=t)
+    state = lambda: new(B, H, dk, dv, t=torch.float32)
+    rows = dict(q=new(B, L, H, dk), k=new(B, L, KV, dk), v=new(B, L, KV, dv))
+    d = S.make_linattn_dims(*rows.values(), 0.5)
+    g, lens, o = new(H, t=torch.float32), new(B, t=torch.int32), new(B, L, H, dv)
+    ws = torch.zeros(64, dtype=torch.uint8)
+    calls = {
+        "swimba_linattn_fwd": dict(**rows, log_decay=g, lens=lens, S0=state(), o=o, S_final=state()),
+        "swimba_linattn_bwd": dict(**rows, log_decay=g, lens=lens, S0=state(), g_o=o, g_S=state(),
+                                   **{"d" + n: x.clone() for n, x in rows.items()}, dS0=state()),
+    }
+    one = {n: x[:, :1].contiguous() for n, x in rows.items()}
+    calls["swimba_linattn_step"] = dict(**one, log_decay=g, S_in=state(), o=o[:, :1].contiguous(), S_out=state())
+    for name, a in calls.items():
+        step = name.endswith("step")
+        dims = S.make_linattn_dims(*one.values(), 0.5) if step else d
+        tail = () if step else (ws, 64)
+        call = lambda **kw: getattr(S, name)(dims, *{**a, **kw}.values(), *tail, 0)
+        assert call() == 0
+        for n, x in a.items():
+            for bad in _others(x):
+                assert call(**{n: bad}) == INVALID, (name, n, bad.shape, bad.dtype)
+    # a workspace is no longer than it is
+    taken.args = None
+    assert S.swimba_linattn_fwd(d, *calls["swimba_linattn_fwd"].values(), ws, 1 << 30, 0) == 0 and taken.args[-2] == 64
+
+
+@pytest.mark.parametrize("io,res_t", [(torch.float32, torch.bfloat16), (torch.bfloat16, torch.float32)])
+def test_norm_tensors_have_the_dims_types_and_sizes(S, taken, io, res_t):
+    rows, width = 6, 32
+    row = lambda t: torch.zeros(rows, width, dtype=t)
+    d = S.make_norm_dims(row(io), row(res_t))
+    types = dict(y=io, z=io, w_post=None, res=res_t, w_pre=None, h=res_t, n=io, g_h=res_t, g_n=io, dy=io, dz=io,
+                 dres=res_t, dw_post=None, dw_pre=None)
+    x = {n: torch.zeros(width) if t is None else row(t) for n, t in types.items()}
+    ws = torch.zeros(64, dtype=torch.uint8)
+    fwd = lambda **kw: S.swimba_block_norm_fwd(d, *({**x, **kw}[n] for n in NORM_FWD), 0)
+    bwd = lambda **kw: S.swimba_block_norm_bwd(d, *({**x, **kw}[n] for n in NORM_BWD), ws, 1 << 30, 0)
+    for names, call in ((NORM_FWD, fwd), (NORM_BWD, bwd)):
+        assert call() == 0
+        for n in names:
+            for bad in _others(x[n]):
+                assert call(**{n: bad}) == INVALID, (n, bad.shape, bad.dtype)
+    assert bwd() == 0 and taken.args[-2] == 64
+
+
+def test_makers_of_dims_refuse_other_types_and_ranks(S):
+    half = torch.zeros(2, 5, 4, 16, dtype=torch.float16)
+    for bad in (half, half.float()[0]):
+        with pytest.raises(S.SwimbaError):
+            S.make_linattn_dims(bad, bad, bad, 1.0)
+    for y, h in ((half, half.float()), (half.float(), half)):
+        with pytest.raises(S.SwimbaError):
+            S.make_norm_dims(y, h)
