@@ -266,6 +266,7 @@ __global__ void __launch_bounds__(256) la_step_kernel(LaStream q, LaStream k, La
                                                       const float* S_in, IO* o, float* S_out, int H, int dk, int dv,
                                                       int cols, float scale) {
   __shared__ float sq[128], sk[128];
+  __shared__ LaDecay decay;
   __shared__ __align__(16) float red[1024];
   const int64_t bh = blockIdx.x;
   const int b = (int)(bh / H), h = (int)(bh % H), tid = threadIdx.x, first = blockIdx.y * cols;
@@ -276,8 +277,9 @@ __global__ void __launch_bounds__(256) la_step_kernel(LaStream q, LaStream k, La
     sq[tid] = to_f32(la_row<IO>(q, b, 0, h, dk)[tid]) * scale;
     sk[tid] = to_f32(la_row<IO>(k, b, 0, h, dk)[tid]);
   }
-  const float gamma = la_pow(g[h] * kLog2e, 1);
+  if (tid == 255) decay = la_decay(g[h], 1);  // (in every thread, 64 x 32 heads of 64 x 64 took 22.2 us in place of 21.4)
   __syncthreads();
+  const LaDecay gamma = decay;
   if (r0 < R) {
     const IO* vp = la_row<IO>(v, b, 0, h, dv) + first + 4 * c;
     const float4 vv = make_float4(to_f32(vp[0]), to_f32(vp[1]), to_f32(vp[2]), to_f32(vp[3]));
@@ -293,10 +295,10 @@ __global__ void __launch_bounds__(256) la_step_kernel(LaStream q, LaStream k, La
         const int j = j0 + i * R;
         if (j >= dk) break;
         const float kj = sk[j], qj = sq[j];
-        s[i].x = fmaf(gamma, s[i].x, kj * vv.x);
-        s[i].y = fmaf(gamma, s[i].y, kj * vv.y);
-        s[i].z = fmaf(gamma, s[i].z, kj * vv.z);
-        s[i].w = fmaf(gamma, s[i].w, kj * vv.w);
+        s[i].x = fmaf(gamma.hi, s[i].x, fmaf(gamma.lo, s[i].x, kj * vv.x));
+        s[i].y = fmaf(gamma.hi, s[i].y, fmaf(gamma.lo, s[i].y, kj * vv.y));
+        s[i].z = fmaf(gamma.hi, s[i].z, fmaf(gamma.lo, s[i].z, kj * vv.z));
+        s[i].w = fmaf(gamma.hi, s[i].w, fmaf(gamma.lo, s[i].w, kj * vv.w));
         acc.x = fmaf(qj, s[i].x, acc.x);
         acc.y = fmaf(qj, s[i].y, acc.y);
         acc.z = fmaf(qj, s[i].z, acc.z);

@@ -58,6 +58,19 @@ struct LaParams {
 // γ^e = exp2(lg e) for e >= 0; γ^0 = 1 also for lg = -inf (a head that keeps nothing).
 __device__ __forceinline__ float la_pow(float lg, int e) { return e == 0 ? 1.f : exp2f(lg * (float)e); }
 
+// γ^e as hi + lo, for a factor that a state meets again and again: rounded once, a γ near 1 is off by up to 2^-25
+// at every use, with the same sign (4096 single tokens at a log decay of -1e-5: 6e-5 of the state; with lo 1e-8).
+// A γ^e below e^-1/2 is forgotten within a few uses.
+struct LaDecay {
+  float hi, lo;
+};
+__device__ __forceinline__ LaDecay la_decay(float g, int e) {
+  const float x = g * (float)e;
+  if (!(fabsf(x) < 0.5f)) return {la_pow(g * kLog2e, e), 0.f};
+  const float m = expm1f(x), hi = 1.f + m;
+  return {hi, m - (hi - 1.f)};  // exact: |m| < 1
+}
+
 __device__ __forceinline__ int64_t la_len(const LaParams& p, int b) {
   if (p.lens == nullptr) return p.L;
   const int64_t n = p.lens[b];

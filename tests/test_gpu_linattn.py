@@ -299,3 +299,30 @@ def test_offsets_past_32_bits(S):
     c.q, c.k, c.v = views
     got = c.forward(S)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# Log decays whose γ and γ^128 lie far from the fp32 number next to them (0.05 to 0.5 of its last place), and slow enough
+# that a state outlives thousands of tokens. Larger than a state's own last place: what a slower decay takes from
+# an fp32 state at a token is lost in its rounding.
+SLOW = [-1.0e-5, -2.3e-5, -2.0 ** -12 * 1.01, -3.3e-4]
+
+
+def mean_drift(got, start, g, n):
+    """Per head, the mean over its elements of the error of a state that only decayed, relative to the state. An
+    update rounds each element by at most 2^-24 of it, to either side: over the 4096 elements or more of a head the
+    mean of 4096 updates' roundings has a standard deviation below 2^-24 64 / 64 = 2^-24. The decays' own error is
+    2^-23 of the whole exponent (at most 2 here). 2^-20 is beyond both; γ rounded to fp32 leaves n 2^-27 or more."""
+    want = start.double() * torch.exp(g.double() * n)[None, :, None, None]
+    return ((got.double() - want) / want).mean(dim=(0, 2, 3)).abs().max().item()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_single_tokens_keep_the_decay(S, dtype):
+    """4096 tokens of zero keys: the state is its start times exp(4096 log_decay)."""
+    c = Case(12, 2, 1, len(SLOW), len(SLOW), 64, 64, dtype, decay=torch.tensor(SLOW))
+    c.k.zero_()
+    start = 1 + torch.rand_like(c.S0)
+    state, o, d = start.clone(), torch.empty(2, 1, len(SLOW), 64, device="cuda", dtype=c.t), c.dims(S)
+    for _ in range(4096):
+        S.check(S.swimba_linattn_step(d, c.q, c.k, c.v, c.g, state, o, state))
+    assert mean_drift(state, start, c.g, 4096) < 2.0 ** -20
