@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(128) la_chain_kernel(const __grid_constant__ L
   const int e = (blockIdx.y * 128 + threadIdx.x) * 4;
   if (e >= size) return;
   const int j = e / dw, c = e - j * dw, sj = r.sj, sc = r.sc;
-  const float lg = p.g[h] * kLog2e, g_all = la_pow(lg, p.cps * p.chunk);
+  const LaDecay g_all = la_decay(p.g[h], p.cps * p.chunk);
   const int64_t len = la_len(p, b);
   float4* seg = reinterpret_cast<float4*>(r.seg + (int64_t)bh * nseg * size + e);
   const int64_t own = (int64_t)bh * size + (int64_t)j * sj + (int64_t)c * sc;
@@ -191,11 +191,11 @@ __global__ void __launch_bounds__(128) la_chain_kernel(const __grid_constant__ L
         const int n = (int)(min((int64_t)c1 * p.chunk, len) - min((int64_t)c0 * p.chunk, len));
         seg[(int64_t)(s0 + i) * (size / 4)] = m;
         if (n > 0) {
-          const float g = n == p.cps * p.chunk ? g_all : la_pow(lg, n);
-          m.x = fmaf(g, m.x, end[i].x);
-          m.y = fmaf(g, m.y, end[i].y);
-          m.z = fmaf(g, m.z, end[i].z);
-          m.w = fmaf(g, m.w, end[i].w);
+          const LaDecay g = n == p.cps * p.chunk ? g_all : la_decay(p.g[h], n);
+          m.x = fmaf(g.hi, m.x, fmaf(g.lo, m.x, end[i].x));
+          m.y = fmaf(g.hi, m.y, fmaf(g.lo, m.y, end[i].y));
+          m.z = fmaf(g.hi, m.z, fmaf(g.lo, m.z, end[i].z));
+          m.w = fmaf(g.hi, m.w, fmaf(g.lo, m.w, end[i].w));
         }
       }
     }

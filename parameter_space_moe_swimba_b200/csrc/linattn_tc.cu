@@ -8,7 +8,7 @@
 // A reverse role mirrors the exponents: γ^(s-i) for s >= i, γ^(n-1-i), γ^(s+1).
 //
 // Persistent, one CTA per SM; an item is one (role, segment, sequence, head), its chunks in order:
-//   warp 0       TMA loads of the X, Y, W tiles into a ring each; the item's table of powers of γ
+//   warp 0       TMA loads of the X, Y, W tiles into a ring each; the item's table of powers of γ; every chunk's γ^n
 //   warp 1       the MMAs of scores, readout and outputs
 //   warp 2       the MMAs of U. (A wait costs an issuing warp about 170 cycles and a commit 70, as much as
 //                two and one of these MMAs, and few MMAs queue up: one warp for both made every wait
@@ -99,7 +99,11 @@ struct LaSmem {
   static constexpr int BAR = POW + 2 * kTable * 4;  // barriers
   static constexpr int NBAR = 2 * NX + 2 * NY + 4 * NW + 6 + 2 * RING + 2 * NU + 4 + 2 + 2;
   static constexpr int MISC = BAR + NBAR * 8;
-  static constexpr int BYTES = MISC + 16;
+  // γ^n of the chunks in flight. A W tile is loaded where the outputs NW chunks before it (MODE 1: U) are done, so
+  // where the state of NW + 1 (NW + 2) chunks before it is: that many factors are in use.
+  static constexpr int FACTORS = 8, FACTOR = MISC + 16;
+  static_assert(NW + 2 <= FACTORS);
+  static constexpr int BYTES = FACTOR + FACTORS * 4;
   // Registers per thread of the six warpgroups (0-3, 4-7 and 8-11, 12-15, 16-19 and 20-23). A spill in one of
   // the chunk loops costs several percent.
   static constexpr int REG_UTIL = DX == 128 ? 48 : DW == 128 ? 72 : 48, REG_PO = DX == 128 ? 64 : DW == 128 ? 72 : 80,
@@ -153,6 +157,7 @@ struct LaItem {
   int role, b, h, seg, c0, c1, rev, len;
   int third;  // γ w's third part counts where at most so many tokens follow (-1: nowhere)
   int64_t bh;
+  int at;  // chunks of the sequence (or segment) that the walk has behind it
   bool begins, ends;  // the state before it is given (else handed over); the state after it is the end's (else to be handed over)
 };
 
@@ -196,6 +201,7 @@ __device__ __forceinline__ bool la_item(const LaTcArgs& a, uint32_t k, LaItem& t
   t.begins = p0 == 0;
   t.ends = p1 == 0xffffffffu;
   const int n = t.c1 - t.c0, a0 = (int)p0, a1 = t.ends ? n : (int)p1;
+  t.at = a0;
   t.c1 = t.c0 + (t.rev ? n - a0 : a1);
   t.c0 = t.c0 + (t.rev ? n - a1 : a0);
   return true;
@@ -321,8 +327,13 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         const CUtensorMap* map = a.map[t.role];
         const int hx = t.h / t.r->x.div, hy = t.h / t.r->y.div, hw = t.h / t.r->w.div;
         if (!(ok = wait(&pw_empty[ii & 1], ((ii >> 1) & 1) ^ 1))) break;
+        // γ^128 = hi + lo: the j-th chunk's factor is hi or hi ± 2^-24, whichever keeps the product of all factors
+        // next to γ's power (rounded once, 512 chunks at a slow decay would put 1.5e-5 into the state; so 1e-7). It
+        // is a function of j, whichever CTA has the chunk.
+        const float lg = p.g[t.h] * kLog2e;
+        const LaDecay g_all = la_decay(p.g[t.h], kLaChunk);
+        const float slip = g_all.lo * 0x1p24f;
         {
-          const float lg = p.g[t.h] * kLog2e;
           float* table = reinterpret_cast<float*>(sm + SM::POW) + (ii & 1) * kTable;
           for (int e = lane; e < kTable; e += 32) {
             const int d = t.rev ? kLaChunk - 1 - e : e - 32;
@@ -333,14 +344,19 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         }
         for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
           int t0;
-          la_chunk(t, i, t0);
+          const int n = la_chunk(t, i, t0);
+          const float j = (float)(t.at + i);
+          const float g = n < kLaChunk ? la_pow(lg, n) : fmaf(rintf((j + 1.f) * slip) - rintf(j * slip), 0x1p-24f, g_all.hi);
           auto load = [&](int boxes, int at, const CUtensorMap* m, uint64_t* bar, int head) {
             mbar_arrive_expect_tx(bar, boxes * kTile);
             for (int k = 0; k < boxes; ++k) tma_load_4d(sm + at + k * kTile, m, bar, 64 * k, head, t0, t.b);
           };
           // in the order in which the tiles come free
           if (!(ok = wait(&w_empty[it % NW], ((it / NW) & 1) ^ 1))) break;
-          if (elect_one()) load(SM::WB, SM::W + (it % NW) * SM::TW, &map[kMapW], &w_full[it % NW], hw);
+          if (elect_one()) {
+            *reinterpret_cast<volatile float*>(sm + SM::FACTOR + it % SM::FACTORS * 4) = g;
+            load(SM::WB, SM::W + (it % NW) * SM::TW, &map[kMapW], &w_full[it % NW], hw);
+          }
           if (!(ok = wait(&y_empty[it % NY], ((it / NY) & 1) ^ 1))) break;
           if (elect_one()) load(SM::XB, SM::Y + (it % NY) * SM::TY, &map[kMapY], &y_full[it % NY], hy);
           if (MODE == 0) {
@@ -635,7 +651,6 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
     bool ok = true;
     for (LaItem t; ok && la_item(a, ii, t); ++ii) {
       const LaRole& r = *t.r;
-      const float lg = p.g[t.h] * kLog2e, g_all = la_pow(lg, kLaChunk);
       const int dx = r.dx, dw = r.dw;
       const int64_t size = (int64_t)dx * dw;
       float m[DX];
@@ -676,12 +691,11 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
           if (it > 0 && !(ok = wait(mx_full, (it & 1) ^ 1))) break;
           copy();
         }
-        int t0;
-        const int n = la_chunk(t, i, t0);
-        const float g = n == kLaChunk ? g_all : la_pow(lg, n);
         const uint32_t ub = it % SM::NU;
         if (!(ok = wait(&u_full[ub], (it / SM::NU) & 1))) break;
         tc_fence_after();
+        // written before W's copy was issued, which U has waited for
+        const float g = lds1(smem_u32(sm) + SM::FACTOR + it % SM::FACTORS * 4);
         if (wq == 0 && lane == 0) {
           mbar_arrive(&y_empty[it % NY]);
           mbar_arrive(MODE == 0 ? &w_read[it % NW] : &w_empty[it % NW]);

@@ -326,3 +326,24 @@ def test_many_single_tokens_keep_the_decay(S, dtype):
     for _ in range(4096):
         S.check(S.swimba_linattn_step(d, c.q, c.k, c.v, c.g, state, o, state))
     assert mean_drift(state, start, c.g, 4096) < 2.0 ** -20
+
+
+@pytest.mark.parametrize("dtype,H,L", [("bf16", 3, 32768), ("bf16", 150, 32768), ("bf16", 150, 32700), ("f32", 3, 32768)])
+def test_long_sequences_keep_the_decay(S, dtype, H, L):
+    """Zero keys leave S_final = exp(L log_decay) S0, zero g_o leaves dS0 = exp(L log_decay) g_S: over segments (3
+    heads), and over 256 chunks in a row in whole and cut sequences (150 heads)."""
+    t, d = (torch.bfloat16 if dtype == "bf16" else torch.float32), 64
+    g = torch.tensor([-1.0e-5, -1.728e-5, -1.97e-5, -2.4557e-5, -4.6393e-5, -5.3672e-5], device="cuda")
+    g = g.repeat(H // 6 + 1)[:H].contiguous()
+    q, k = torch.ones(1, L, H, d, device="cuda", dtype=t), torch.zeros(1, L, H, d, device="cuda", dtype=t)
+    dims = S.make_linattn_dims(q, k, k, 1.0)
+    start, end, o = 1 + torch.rand(1, H, d, d, device="cuda"), torch.empty(1, H, d, d, device="cuda"), torch.empty_like(q)
+    ws = S.new_linattn_workspace(dims, S.SWIMBA_OP_LINATTN_FWD)
+    S.check(S.swimba_linattn_fwd(dims, q, k, k, g, None, start, o, end, ws, ws.numel()))
+    assert S.swimba_get_device_status(ws) == 0
+    assert mean_drift(end, start, g, L) < 2.0 ** -20
+    ws = S.new_linattn_workspace(dims, S.SWIMBA_OP_LINATTN_BWD)
+    grads = [torch.empty_like(q) for _ in range(3)]
+    S.check(S.swimba_linattn_bwd(dims, q, k, k, g, None, None, k, start, *grads, end, ws, ws.numel()))
+    assert S.swimba_get_device_status(ws) == 0
+    assert mean_drift(end, start, g, L) < 2.0 ** -20
