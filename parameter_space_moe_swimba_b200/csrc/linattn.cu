@@ -340,24 +340,42 @@ swimba_status check_la(const swimba_linattn_dims* d) {
   return SWIMBA_OK;
 }
 
+// The tensor-core kernel takes roles of one padded size (64 or 128) together: all three where d_k and
+// d_v pad alike, else dq and dk, then dv.
+bool la_one_launch(int roles, int d_k, int d_v) { return roles < 3 || (d_k <= 64) == (d_v <= 64); }
+
 // Segments per sequence. Splitting a sequence costs a second pass over y and w (the segments' end
 // states), so it pays only where the heads alone leave SMs idle. The rule takes the split with the
-// least time in units of one chunk's outputs on one CTA: rounds of CTAs x chunks per segment, with
-// `pass` units more per chunk for the state pass of a split sequence, `state` per segment for its
-// state's way through memory and `launch` for the two launches more. Tensor cores (a unit is about 3 us):
+// least time in units of one chunk's outputs on one CTA, summed over the launches: rounds of CTAs x chunks per
+// segment, with `pass` units more per chunk for the state pass of a split sequence, `state` per segment for its
+// state's way through memory and `launch` for the launches more. Tensor cores (a unit is about 3 us):
 // 16 heads x 65536 tokens take 0.39 ms in 9 segments, 2.1 ms whole. fp32 (32 tokens, 8 us): 48 roles x
-// 333 tokens take 76 us in segments, 176 us whole. Fewer heads than SMs are never cut between two CTAs.
-LaPlan la_plan(const swimba_linattn_dims* d, int roles, bool tc) {
+// 333 tokens take 76 us in segments, 176 us whole. Gradients in two launches, heads of 64 x 128, 4096 tokens:
+// 24 heads take 138 us in 6 segments, 32 heads 165 in 4 and 192 whole, 40 heads 208 in 3 and 194 whole.
+// Whole sequences of as many heads as CTAs or more are dealt out in equal shares where that is less (see run_la_tc),
+// unless they have lengths of their own: 160 heads of 128 x 16384 tokens take 0.59 ms so, 1.04 ms in 8 segments.
+LaPlan la_plan(const swimba_linattn_dims* d, int roles, bool tc, bool lens) {
   const int chunk = tc ? kLaChunk : kLaSimtChunk;
   const int64_t nch = (d->seqlen + chunk - 1) / chunk;
-  const int64_t heads = d->batch * d->n_heads * roles * (tc ? 1 : (std::max(d->d_k, d->d_v) + kSimtCols - 1) / kSimtCols);
+  const int64_t heads = d->batch * d->n_heads * (tc ? 1 : (std::max(d->d_k, d->d_v) + kSimtCols - 1) / kSimtCols);
   const int64_t slots = tc ? kSMs : 4 * kSMs;
-  const double pass = tc ? 0.5 : 0.7, state = tc ? 2 : 0.3, launch = tc ? 4 : 0.7;
-  LaPlan best{tc, 1, (int)nch, tc && heads >= kSMs};
-  double least = (double)((heads + slots - 1) / slots) * nch;
+  const bool one = !tc || la_one_launch(roles, d->d_k, d->d_v);
+  const double pass = tc ? 0.5 : 0.7, state = tc ? 2 : 0.3, launch = !tc ? 0.7 : one ? 4 : 13;
+  const bool cut = tc && !lens && heads * (one ? roles : 2) >= kSMs;
+  auto units = [&](int64_t items, int64_t segs, int64_t cps) {
+    const double whole = (double)((items * segs + slots - 1) / slots);
+    if (segs > 1) return whole * (cps * (1 + pass) + state);
+    return cut && items >= kSMs ? std::min(whole * cps, la_shared_units(items * cps, kSMs)) : whole * cps;
+  };
+  auto time = [&](int64_t segs, int64_t cps) {
+    const double t = one ? units(heads * roles, segs, cps) : units(heads * 2, segs, cps) + units(heads, segs, cps);
+    return segs > 1 ? t + launch : t;
+  };
+  LaPlan best{tc, 1, (int)nch, cut};
+  double least = time(1, nch);
   for (int64_t n = 2; n <= std::min<int64_t>(nch, 64); ++n) {
     const int64_t cps = (nch + n - 1) / n, segs = (nch + cps - 1) / cps;
-    const double t = (double)((heads * segs + slots - 1) / slots) * (cps * (1 + pass) + state) + launch;
+    const double t = time(segs, cps);
     if (t < least) {
       least = t;
       best = LaPlan{tc, (int)segs, (int)cps, false};
@@ -431,11 +449,8 @@ cudaError_t run_simt(const LaParams& p, cudaStream_t s) {
   return dx <= 96 ? launch_simt<IO, 6>(p, dw, s) : launch_simt<IO, 8>(p, dw, s);
 }
 
-// The tensor-core kernel takes roles of one padded size (64 or 128) together: all three where d_k and
-// d_v pad alike, else dq and dk, then dv.
 cudaError_t run_tc(const LaParams& p, cudaStream_t s) {
-  auto pad = [](int d) { return d <= 64 ? 64 : 128; };
-  const bool same = p.n_roles < 3 || pad(p.role[2].dx) == pad(p.role[2].dw);
+  const bool same = la_one_launch(p.n_roles, p.role[0].dx, p.role[0].dw);
   LaParams part[2] = {p, p};
   if (!same) {
     part[0].n_roles = 2;
@@ -500,7 +515,9 @@ extern "C" {
 size_t swimba_linattn_workspace_size(const swimba_linattn_dims* dims, int op) {
   if (check_la(dims) != SWIMBA_OK || (op != SWIMBA_OP_LINATTN_FWD && op != SWIMBA_OP_LINATTN_BWD)) return 0;
   const int roles = op == SWIMBA_OP_LINATTN_FWD ? 1 : 3;
-  return la_layout(dims, la_plan(dims, roles, la_use_tc(dims)), roles).total;
+  const bool tc = la_use_tc(dims);  // enough for a call with lens and for one without
+  return std::max(la_layout(dims, la_plan(dims, roles, tc, true), roles).total,
+                  la_layout(dims, la_plan(dims, roles, tc, false), roles).total);
 }
 
 swimba_status swimba_linattn_fwd(const swimba_linattn_dims* dims, const void* q, const void* k, const void* v,
@@ -509,7 +526,7 @@ swimba_status swimba_linattn_fwd(const swimba_linattn_dims* dims, const void* q,
   const swimba_status st = check_la(dims);
   if (st != SWIMBA_OK) return st;
   if (!q || !k || !v || !log_decay || !o || o == q || o == k || o == v) return SWIMBA_ERR_INVALID_ARG;
-  const LaPlan pl = la_plan(dims, 1, la_use_tc(dims));
+  const LaPlan pl = la_plan(dims, 1, la_use_tc(dims), lens != nullptr);
   const LaLayout l = la_layout(dims, pl, 1);
   if (ws == nullptr || ws_bytes < l.total) return SWIMBA_ERR_WORKSPACE;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(S0) || !aligned16(S_final) ||
@@ -579,7 +596,7 @@ swimba_status swimba_linattn_bwd(const swimba_linattn_dims* dims, const void* q,
       if (out[i] == in[j]) return SWIMBA_ERR_INVALID_ARG;
     if (out[i] == out[(i + 1) % 3]) return SWIMBA_ERR_INVALID_ARG;
   }
-  const LaPlan pl = la_plan(dims, 3, la_use_tc(dims));
+  const LaPlan pl = la_plan(dims, 3, la_use_tc(dims), lens != nullptr);
   const LaLayout l = la_layout(dims, pl, 3);
   if (ws == nullptr || ws_bytes < l.total) return SWIMBA_ERR_WORKSPACE;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(g_o) || !aligned16(dq) || !aligned16(dk) ||

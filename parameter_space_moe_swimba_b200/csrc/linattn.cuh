@@ -92,6 +92,9 @@ struct LaPlan {
   bool cut;       // sequences may be cut between two CTAs (see run_la_tc): room for the states handed over
 };
 
+// Chunks of the longest of `ctas` equal shares of `total` chunks, and 3 for cutting sequences between them.
+inline double la_shared_units(int64_t total, int ctas) { return (double)(total / ctas + 3); }
+
 constexpr int kLaCtas = 148;  // one per SM
 constexpr size_t kLaHandBytes = (size_t)kLaCtas * 128 * 128 * 4;
 constexpr size_t kLaFlagBytes = 1024;

@@ -887,7 +887,7 @@ cudaError_t run_la_tc(const LaParams& p, bool states, cudaStream_t s) {
   a.share = (uint32_t)(total / sms);
   a.extra = (uint32_t)(total % sms);
   a.p.balanced = !states && p.hand_flags != nullptr && p.nseg == 1 && p.lens == nullptr && a.items >= (uint32_t)sms &&
-                 total < (1u << 31) && rounds * p.cps > total / sms + 3;
+                 total < (1u << 31) && (double)(rounds * p.cps) > la_shared_units((int64_t)total, sms);
   if (a.p.balanced) {
     const cudaError_t e = cudaMemsetAsync(p.hand_flags, 0, kLaFlagBytes, s);
     if (e != cudaSuccess) return e;

@@ -347,3 +347,37 @@ def test_long_sequences_keep_the_decay(S, dtype, H, L):
     S.check(S.swimba_linattn_bwd(dims, q, k, k, g, None, None, k, start, *grads, end, ws, ws.numel()))
     assert S.swimba_get_device_status(ws) == 0
     assert mean_drift(end, start, g, L) < 2.0 ** -20
+
+
+@pytest.mark.parametrize("H,L", [(149, 16384), (160, 16384), (175, 20000)])
+def test_more_heads_than_sms_stay_whole(S, H, L):
+    """Long sequences of a few more heads than SMs go in equal shares and not through segments, which read keys and
+    values twice: one launch, and the results that the same heads give in calls of fewer, which go another way."""
+    c = Case(13, 1, 1, H, H, 16, 8, "bf16", decay=-torch.exp2(torch.linspace(-1, -14, H)))
+    g = torch.Generator(device="cuda")
+    g.manual_seed(14)
+    q, k, v = (torch.randn(1, L, H, d, generator=g, device="cuda").bfloat16() for d in (16, 16, 8))
+
+    def forward(first, last):
+        x = [t[:, :, first:last].contiguous() for t in (q, k, v)]
+        S0, decay = c.S0[:, first:last].contiguous(), c.g[first:last].contiguous()
+        d = S.make_linattn_dims(*x, 0.25)
+        ws = S.new_linattn_workspace(d, S.SWIMBA_OP_LINATTN_FWD)
+        o, end = torch.empty_like(x[2]), torch.empty_like(S0)
+        before = S.swimba_kernel_launches()
+        S.check(S.swimba_linattn_fwd(d, *x, decay, None, S0, o, end, ws, ws.numel()))
+        assert S.swimba_get_device_status(ws) == 0
+        return o, end, S.swimba_kernel_launches() - before
+
+    o, end, launches = forward(0, H)
+    assert launches == 1
+    for first in range(0, H, 100):
+        part, part_end, _ = forward(first, min(first + 100, H))
+        # the two ways differ in where fp32 sums are cut: the states by roundings of their own size, the outputs
+        # where such a difference crosses a bf16 rounding of the scores, of the state's copy or of the output
+        got, want = o[:, :, first:first + 100].float(), part.float()
+        size = want.square().mean().sqrt()
+        assert (got - want).abs().max() <= 2.0 ** -8 * (want.abs() + 4 * size).max()
+        assert (got - want).square().mean().sqrt() <= 2.0 ** -10 * size
+        state = part_end.square().mean().sqrt()
+        assert (end[:, first:first + 100] - part_end).abs().max() <= 2.0 ** -17 * (part_end.abs().max() + state)
