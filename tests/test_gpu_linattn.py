@@ -381,3 +381,31 @@ def test_more_heads_than_sms_stay_whole(S, H, L):
         assert (got - want).square().mean().sqrt() <= 2.0 ** -10 * size
         state = part_end.square().mean().sqrt()
         assert (end[:, first:first + 100] - part_end).abs().max() <= 2.0 ** -17 * (part_end.abs().max() + state)
+
+
+# Sizes that pad differently (other instances of the kernel; gradients in two launches), in segments and in shares.
+UNEVEN = {
+    "split_64x128": dict(B=1, L=1500, H=1, KV=1, dk=64, dv=128),
+    "split_128x64": dict(B=1, L=1500, H=1, KV=1, dk=128, dv=64, start=False),
+    "split_lens_72x40": dict(B=2, L=1700, H=2, KV=1, dk=72, dv=40, lens=[1430, 400]),
+    "split_lens_24x104": dict(B=3, L=1700, H=2, KV=2, dk=24, dv=104, lens=[1537, 0, 129], fused=True),
+    "cut_16x72": dict(B=1, L=900, H=149, KV=149, dk=16, dv=72),
+    "cut_72x16_shared": dict(B=1, L=700, H=150, KV=50, dk=72, dv=16),
+}
+
+
+@pytest.mark.parametrize("name", UNEVEN)
+def test_uneven_head_sizes_in_segments_and_shares(S, name):
+    c = Case(15, dtype="bf16", **UNEVEN[name])
+    B, L, H, KV, dk, dv = c.shape
+    o, S_final = c.forward(S, torch.zeros(B, L, H, dv, device="cuda", dtype=c.t))
+    a = c.np
+    r = M.linattn_forward(a["q"], a["k"], a["v"], a["g"], c.scale, c.np_lens, a["S0"])
+    c.close(Case.f64(o), r.out, r.once, r.mag, "o")
+    c.close(Case.f64(S_final), r.M, None, r.M_mag, "S_final", out=False)
+    dq, dk, dv, dS0 = (Case.f64(x) for x in c.backward(S))
+    rq, rk, rv = M.linattn_backward(a["q"], a["k"], a["v"], a["g"], c.scale, a["g_o"], c.np_lens, a["S0"], a["g_S"])
+    c.close(dq, rq.out, rq.once, rq.mag, "dq")
+    for got, r, what in ((dk, rk, "dk"), (dv, rv, "dv")):
+        c.close(got, *(M.sum_shared(x, KV) for x in (r.out, r.once, r.mag)), what)
+    c.close(dS0, rv.M, None, rv.M_mag, "dS0", out=False)
