@@ -409,3 +409,21 @@ def test_uneven_head_sizes_in_segments_and_shares(S, name):
     for got, r, what in ((dk, rk, "dk"), (dv, rv, "dv")):
         c.close(got, *(M.sum_shared(x, KV) for x in (r.out, r.once, r.mag)), what)
     c.close(dS0, rv.M, None, rv.M_mag, "dS0", out=False)
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (64, 128)])
+def test_gradients_of_cut_sequences_are_those_of_whole_ones(S, dk, dv):
+    """160 heads make 480 pieces of work, in equal shares over the SMs; 40 heads 120, fewer than there are SMs, which
+    are never cut: the same bits, the states' gradients included."""
+    c = Case(16, 1, 1900, 160, 160, dk, dv, "bf16", scale=0.1)
+    whole = c.backward(S)
+    for h in range(0, 160, 40):
+        part = Case(16, 1, 1900, 40, 40, dk, dv, "bf16", scale=0.1)
+        cut = lambda x: x[:, :, h:h + 40].contiguous()
+        part.q, part.k, part.v, part.g_o = (cut(x) for x in (c.q, c.k, c.v, c.g_o))
+        part.S0, part.g_S = c.S0[:, h:h + 40].contiguous(), c.g_S[:, h:h + 40].contiguous()
+        part.g = c.g[h:h + 40].contiguous()
+        *grads, dS0 = part.backward(S)
+        for got, want in zip(whole, grads):
+            assert torch.equal(cut(got), want)
+        assert torch.equal(whole[3][:, h:h + 40], dS0)
