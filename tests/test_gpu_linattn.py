@@ -427,3 +427,57 @@ def test_gradients_of_cut_sequences_are_those_of_whole_ones(S, dk, dv):
         for got, want in zip(whole, grads):
             assert torch.equal(cut(got), want)
         assert torch.equal(whole[3][:, h:h + 40], dS0)
+
+
+def two_part_loss(w, v):
+    """What of the fp32 product w v its first two truncated bf16 parts leave out, relative to the product."""
+    top = lambda x: (x.view(np.uint32) & np.uint32(0xffff0000)).view(np.float32)
+    x = (np.float32(w) * v).astype(np.float32)
+    rest = x - top(x)
+    return (rest - top(rest)) / x
+
+
+@pytest.mark.parametrize("L,at", [(32, 0), (672, 0), (672, 640), (1536, 0), (1536, 1504)])
+def test_states_hold_24_bits(S, L, at):
+    """S_final and dS0 from values whose decayed products need all 24 bits: of every bf16 in [1, 2) the one whose product
+    loses most in two parts. 32 tokens of them stand at the sequence's beginning or end, zeros elsewhere; all
+    terms have one sign, so that what is lost adds up. (The longest go in segments.)
+    Tolerance: a power is off by 2 fp32 steps, 2^-22, its factor and the product by 2^-24 each; the 32 tokens are
+    2 steps of 16 of 3 parts each, 6 products whose running sum is kept to 2^-22; 11 chunks or segments more round the state by 2^-24
+    each: 41 2^-24, below 3 2^-20. Two parts would be off by more than twice that."""
+    tol, g, d = 3 * 2.0 ** -20, -1e-3, 64
+    values = (1 + np.arange(128) / 128).astype(np.float32)
+    gd = float(np.float32(g))
+    tokens = np.arange(at, at + 32)
+    in_chunk = tokens % 128
+    size = min(128, L - at // 128 * 128)
+    decay = torch.tensor([g], device="cuda")
+    ones, zeros = torch.ones(1, 1, 1, d, device="cuda").bfloat16(), torch.zeros(1, L, 1, d, device="cuda").bfloat16()
+
+    def stream(weights):
+        """[1, L, 1, d] of the chosen values, and those in fp64; the loss of two parts is past the tolerance."""
+        chosen = np.array([values[np.argmax(two_part_loss(w, values))] for w in weights])
+        lost = np.array([float(two_part_loss(w, v[None])[0]) for w, v in zip(weights, chosen)])
+        assert (lost * weights * chosen).sum() > 2 * tol * (weights * chosen).sum()
+        x = zeros.clone()
+        x[0, tokens, 0] = torch.from_numpy(chosen).cuda().bfloat16()[:, None]
+        return x, chosen.astype(np.float64)
+
+    def near(got, want):
+        assert (got.double() / want - 1).abs().max().item() < tol
+
+    one = zeros.clone()
+    one[0, tokens, 0] = 1
+    v, chosen = stream(np.exp(gd * (size - 1 - in_chunk)).astype(np.float32))
+    dims = S.make_linattn_dims(one, one, v, 1.0)
+    ws = S.new_linattn_workspace(dims, S.SWIMBA_OP_LINATTN_FWD)
+    o, state = torch.empty_like(v), torch.empty(1, 1, d, d, device="cuda")
+    S.check(S.swimba_linattn_fwd(dims, one, one, v, decay, None, None, o, state, ws, ws.numel()))
+    assert S.swimba_get_device_status(ws) == 0
+    near(state, (np.exp(gd * (L - 1 - tokens)) * chosen).sum())
+    g_o, chosen = stream(np.exp(gd * (in_chunk + 1)).astype(np.float32))
+    ws = S.new_linattn_workspace(dims, S.SWIMBA_OP_LINATTN_BWD)
+    grads = [torch.empty_like(v) for _ in range(3)]
+    S.check(S.swimba_linattn_bwd(dims, one, one, v, decay, None, None, g_o, None, *grads, state, ws, ws.numel()))
+    assert S.swimba_get_device_status(ws) == 0
+    near(state, (np.exp(gd * (tokens + 1)) * chosen).sum())
