@@ -7,6 +7,7 @@
 // the recurrence itself is stated in include/swimba.h.
 #include <algorithm>
 #include <cstdio>
+#include <type_traits>
 
 #include "linattn.cuh"
 
@@ -30,13 +31,18 @@ __device__ __forceinline__ const IO* la_row(const LaStream& s, int b, int64_t t,
 // rows (16 i + 4 p + 0..3, p its quarter) of two columns in registers, so a token costs it 3 FMA-pipe
 // operations per state element and one 16-byte shared read of x and of y per 8 of them; the four
 // quarters' partial readouts meet in two shuffles. Bound by the FMA pipe (3 d_x d_w operations per
-// token and head). MODE 0 writes the outputs, MODE 1 only the segment's end state from zero.
+// token and head, 2 where decays are put off). MODE 0 writes the outputs, MODE 1 only the segment's end state from zero.
+// (A count of 4 CTAs for NI = 8 gives it a better order of instructions too: 4 x 1024 tokens of 16 heads backward 920
+// -> 886 us; counts for the others, with their spills or fewer CTAs, cost them up to 40 %.)
 template <typename IO, int NI, int MODE>
-__global__ void __launch_bounds__(128) la_simt_kernel(const __grid_constant__ LaParams p) {
+__global__ void __launch_bounds__(128, NI == 8 ? 4 : 0) la_simt_kernel(const __grid_constant__ LaParams p) {
   __shared__ __align__(16) float sx[kSimtTokens][NI * 16];
   __shared__ __align__(16) float sy[kSimtTokens][NI * 16];
   __shared__ __align__(16) float sw[kSimtTokens][kSimtCols];
   __shared__ __align__(16) float so[MODE == 0 ? kSimtTokens : 1][kSimtCols];
+  __shared__ float later[kSimtTokens + 1], sooner[kSimtTokens + 1];  // γ^e and γ^-e
+  __shared__ float one, slip;                                        // γ and its relative error
+  __shared__ LaDecay all;                                            // γ^kSimtTokens
   const int tid = threadIdx.x, lane = tid & 31, part = lane & 3;
   const int col = (tid >> 5) * 16 + (lane >> 2) * 2;
   int64_t item = blockIdx.x;
@@ -50,8 +56,22 @@ __global__ void __launch_bounds__(128) la_simt_kernel(const __grid_constant__ La
   const int ncol = min(kSimtCols, r.dw - c_base);
   // γ's rounding would grow with every token that a state outlives: `slip`, its relative error, is taken out
   // of the state after every kSimtTokens tokens (without it 4e-6 in place of 3e-7 at 333 tokens).
-  const double exact = exp((double)p.g[h]);
-  const float gamma = (float)exact, slip = gamma > 0.f ? (float)((exact - (double)gamma) / (double)gamma) : 0.f;
+  // Where γ is so near 1 that kSimtTokens tokens take less than 40 % of a state (`lazy`), they leave M as it is, their
+  // values enter it times γ^-e and their readouts leave it times γ^e, and then it decays once, by γ^kSimtTokens's hi
+  // or hi ± 2^-24 as in the tensor-core kernel: a product with γ at every token would be rounded in one direction
+  // (16384 tokens at log decays of -2^-17 to -2^-24: 6e-6 in place of 5e-7).
+  const float g = p.g[h];
+  const bool lazy = fabsf(g) * kSimtTokens < 0.5f;
+  if (tid < 64 && lane <= kSimtTokens) {
+    const bool back = tid >= 32;
+    const double e = exp((double)g * (back ? -lane : lane));
+    const LaDecay d = {(float)e, (float)(e - (double)(float)e)};
+    (back ? sooner : later)[lane] = d.hi;
+    if (!back && lane == 1) one = d.hi, slip = d.hi > 0.f ? d.lo / d.hi : 0.f;
+    if (!back && lane == kSimtTokens) all = d;
+  }
+  __syncthreads();
+  const float gamma = one, slip1 = slip;
   const int64_t len = la_len(p, b);
   int c0, c1;
   la_segment(p, len, seg, r.rev, c0, c1);
@@ -76,61 +96,80 @@ __global__ void __launch_bounds__(128) la_simt_kernel(const __grid_constant__ La
   for (int i = tid; i < kSimtTokens * kSimtCols; i += 128) sw[0][i] = 0.f;
 
   constexpr int V = Vec16<IO>::n;
-  float decay = r.rev ? 1.f : gamma;  // before a token; M is already decayed to a reverse segment's first token
   for (int64_t at = 0; at < hi - lo; at += kSimtTokens) {
     const int n = (int)min((int64_t)kSimtTokens, hi - lo - at);
+    const int before = r.rev && at == 0 ? 0 : 1;  // decays before the first token: a reverse segment's M has had it
     auto token = [&](int i) { return r.rev ? hi - 1 - at - i : lo + at + i; };
     __syncthreads();
-    auto stage = [&](const LaStream& s, float* dst, int pitch, int first, int count, int d, float f) {
+    auto stage = [&](const LaStream& s, float* dst, int pitch, int first, int count, int d, float scale, bool value) {
       const int per = count / V;
       for (int i = tid; i < n * per; i += 128) {
         const int t = i / per, v = (i - t * per) * V;
+        const float f = value && lazy ? scale * sooner[t + before] : scale;
         float f8[V];
         Vec16<IO>::unpack(*reinterpret_cast<const uint4*>(la_row<IO>(s, b, token(t), h, d) + first + v), f8);
 #pragma unroll
         for (int e = 0; e < V; ++e) dst[t * pitch + v + e] = f8[e] * f;
       }
     };
-    if (MODE == 0) stage(r.x, sx[0], NI * 16, 0, r.dx, r.dx, 1.f);
-    stage(r.y, sy[0], NI * 16, 0, r.dx, r.dx, 1.f);
-    stage(r.w, sw[0], kSimtCols, c_base, ncol, r.dw, r.s_u);
+    if (MODE == 0) stage(r.x, sx[0], NI * 16, 0, r.dx, r.dx, 1.f, false);
+    stage(r.y, sy[0], NI * 16, 0, r.dx, r.dx, 1.f, false);
+    stage(r.w, sw[0], kSimtCols, c_base, ncol, r.dw, r.s_u, true);
     __syncthreads();
-    const float slip_n = slip * (float)n;
+    float decay = before ? gamma : 1.f;
+    if (!lazy) {
+      const float slip_n = slip1 * (float)n;
 #pragma unroll
-    for (int i = 0; i < NI * 4; ++i) {
-      M[i][0] = fmaf(M[i][0], slip_n, M[i][0]);
-      M[i][1] = fmaf(M[i][1], slip_n, M[i][1]);
+      for (int i = 0; i < NI * 4; ++i) {
+        M[i][0] = fmaf(M[i][0], slip_n, M[i][0]);
+        M[i][1] = fmaf(M[i][1], slip_n, M[i][1]);
+      }
     }
-    for (int t = 0; t < n; ++t) {
-      const float2 w = *reinterpret_cast<const float2*>(&sw[t][col]);
-      float a0 = 0.f, a1 = 0.f;
+    auto tokens = [&](auto put_off) {
+      for (int t = 0; t < n; ++t) {
+        const float2 w = *reinterpret_cast<const float2*>(&sw[t][col]);
+        float a0 = 0.f, a1 = 0.f;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const float4 y = *reinterpret_cast<const float4*>(&sy[t][16 * i + 4 * part]);
-        const float yv[4] = {y.x, y.y, y.z, y.w};
-        float xv[4] = {};
-        if (MODE == 0) {
-          const float4 x = *reinterpret_cast<const float4*>(&sx[t][16 * i + 4 * part]);
-          xv[0] = x.x, xv[1] = x.y, xv[2] = x.z, xv[3] = x.w;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float* m = M[4 * i + e];
-          m[0] = fmaf(yv[e], w.x, m[0] * decay);
-          m[1] = fmaf(yv[e], w.y, m[1] * decay);
+        for (int i = 0; i < NI; ++i) {
+          const float4 y = *reinterpret_cast<const float4*>(&sy[t][16 * i + 4 * part]);
+          const float yv[4] = {y.x, y.y, y.z, y.w};
+          float xv[4] = {};
           if (MODE == 0) {
-            a0 = fmaf(xv[e], m[0], a0);
-            a1 = fmaf(xv[e], m[1], a1);
+            const float4 x = *reinterpret_cast<const float4*>(&sx[t][16 * i + 4 * part]);
+            xv[0] = x.x, xv[1] = x.y, xv[2] = x.z, xv[3] = x.w;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float* m = M[4 * i + e];
+            m[0] = fmaf(yv[e], w.x, put_off ? m[0] : m[0] * decay);
+            m[1] = fmaf(yv[e], w.y, put_off ? m[1] : m[1] * decay);
+            if (MODE == 0) {
+              a0 = fmaf(xv[e], m[0], a0);
+              a1 = fmaf(xv[e], m[1], a1);
+            }
           }
         }
+        decay = gamma;
+        if (MODE == 0) {
+          a0 += __shfl_xor_sync(0xffffffffu, a0, 1);
+          a1 += __shfl_xor_sync(0xffffffffu, a1, 1);
+          a0 += __shfl_xor_sync(0xffffffffu, a0, 2);
+          a1 += __shfl_xor_sync(0xffffffffu, a1, 2);
+          const float f = put_off ? r.s_inter * later[t + before] : r.s_inter;
+          if (part == 0) *reinterpret_cast<float2*>(&so[t][col]) = make_float2(a0 * f, a1 * f);
+        }
       }
-      decay = gamma;
-      if (MODE == 0) {
-        a0 += __shfl_xor_sync(0xffffffffu, a0, 1);
-        a1 += __shfl_xor_sync(0xffffffffu, a1, 1);
-        a0 += __shfl_xor_sync(0xffffffffu, a0, 2);
-        a1 += __shfl_xor_sync(0xffffffffu, a1, 2);
-        if (part == 0) *reinterpret_cast<float2*>(&so[t][col]) = make_float2(a0 * r.s_inter, a1 * r.s_inter);
+    };
+    if (!lazy) {
+      tokens(std::false_type{});
+    } else {
+      tokens(std::true_type{});
+      const int e = n - 1 + before;
+      const float f = e == kSimtTokens ? la_factor(all, (int)(at / kSimtTokens)) : later[e];
+#pragma unroll
+      for (int i = 0; i < NI * 4; ++i) {
+        M[i][0] *= f;
+        M[i][1] *= f;
       }
     }
     if (MODE == 0) {
@@ -144,8 +183,8 @@ __global__ void __launch_bounds__(128) la_simt_kernel(const __grid_constant__ La
     }
   }
   if (MODE == 0 && (p.nseg > 1 || r.M_end == nullptr)) return;
-  // a reverse segment leaves M decayed to the token before it (`decay` is γ once a token was seen)
-  const float last = r.rev ? decay : 1.f;
+  // a reverse segment leaves M decayed to the token before it
+  const float last = r.rev && hi > lo ? one : 1.f;
   float* end = MODE == 1 ? r.seg + (bh * p.nseg + seg) * r.dx * r.dw : r.M_end + bh * r.dx * r.dw;
   const int ej = MODE == 1 ? r.dw : r.sj, ec = MODE == 1 ? 1 : r.sc;
 #pragma unroll

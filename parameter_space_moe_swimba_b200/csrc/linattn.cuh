@@ -71,6 +71,13 @@ __device__ __forceinline__ LaDecay la_decay(float g, int e) {
   return {hi, m - (hi - 1.f)};  // exact: |m| < 1
 }
 
+// The j-th of a series of factors for hi + lo, 1/2 < hi <= 1: hi or hi ± 2^-24, whichever keeps the product of all of
+// them next to the power. A function of j, so that a series may be taken up anywhere.
+__device__ __forceinline__ float la_factor(LaDecay d, int j) {
+  const float c = d.lo * 0x1p24f;
+  return fmaf(rintf((float)(j + 1) * c) - rintf((float)j * c), 0x1p-24f, d.hi);
+}
+
 __device__ __forceinline__ int64_t la_len(const LaParams& p, int b) {
   if (p.lens == nullptr) return p.L;
   const int64_t n = p.lens[b];

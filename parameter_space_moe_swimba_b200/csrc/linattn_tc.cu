@@ -327,12 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         const CUtensorMap* map = a.map[t.role];
         const int hx = t.h / t.r->x.div, hy = t.h / t.r->y.div, hw = t.h / t.r->w.div;
         if (!(ok = wait(&pw_empty[ii & 1], ((ii >> 1) & 1) ^ 1))) break;
-        // γ^128 = hi + lo: the j-th chunk's factor is hi or hi ± 2^-24, whichever keeps the product of all factors
-        // next to γ's power (rounded once, 512 chunks at a slow decay would put 1.5e-5 into the state; so 1e-7). It
-        // is a function of j, whichever CTA has the chunk.
+        // γ^128, rounded once, would put 1.5e-5 into the state over 512 chunks at a slow decay; in a series of factors
+        // it puts 1e-7.
         const float lg = p.g[t.h] * kLog2e;
         const LaDecay g_all = la_decay(p.g[t.h], kLaChunk);
-        const float slip = g_all.lo * 0x1p24f;
         {
           float* table = reinterpret_cast<float*>(sm + SM::POW) + (ii & 1) * kTable;
           for (int e = lane; e < kTable; e += 32) {
@@ -345,8 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_kernel(const __grid_constan
         for (int i = 0; i < t.c1 - t.c0; ++i, ++it) {
           int t0;
           const int n = la_chunk(t, i, t0);
-          const float j = (float)(t.at + i);
-          const float g = n < kLaChunk ? la_pow(lg, n) : fmaf(rintf((j + 1.f) * slip) - rintf(j * slip), 0x1p-24f, g_all.hi);
+          const float g = n < kLaChunk ? la_pow(lg, n) : la_factor(g_all, t.at + i);
           auto load = [&](int boxes, int at, const CUtensorMap* m, uint64_t* bar, int head) {
             mbar_arrive_expect_tx(bar, boxes * kTile);
             for (int k = 0; k < boxes; ++k) tma_load_4d(sm + at + k * kTile, m, bar, 64 * k, head, t0, t.b);

@@ -481,3 +481,27 @@ def test_states_hold_24_bits(S, L, at):
     S.check(S.swimba_linattn_bwd(dims, one, one, v, decay, None, None, g_o, None, *grads, state, ws, ws.numel()))
     assert S.swimba_get_device_status(ws) == 0
     near(state, (np.exp(gd * (tokens + 1)) * chosen).sum())
+
+
+@pytest.mark.parametrize("B", [2, 148])
+def test_fp32_keeps_decays_next_to_one(S, B):
+    """Decays of which a token takes about one last place of an fp32 state, or fewer: zero keys leave the start times
+    exp(L log_decay), zero g_o the end's gradient times it, over segments (8 heads) and token by token (592 heads).
+    Rounded at every token they would be off by a part of that place each time, all in one direction: 4e-5 of the state.
+    Decayed every 16 tokens, an element's 256 roundings of at most 2^-24 of it may all be alike, but not those
+    of a head's 512 elements or more: their mean has a standard deviation below 256 2^-24 / 22 / 3^0.5 = 4e-7 for 2
+    sequences and 5e-8 for 148, 7 of which are below 3e-6 and 2^-20 with the decays' own 2^-23."""
+    L, d = 4096, 16
+    g = -torch.tensor([1.5 * 2.0 ** -24, 1.3 * 2.0 ** -23, 1.5 * 2.0 ** -22, 2.0 ** -20], device="cuda")
+    H = len(g)
+    q, k = torch.ones(B, L, H, d, device="cuda"), torch.zeros(B, L, H, d, device="cuda")
+    dims = S.make_linattn_dims(q, k, k, 1.0)
+    start, end, o = 1 + torch.rand(B, H, d, d, device="cuda"), torch.empty(B, H, d, d, device="cuda"), torch.empty_like(q)
+    ws = S.new_linattn_workspace(dims, S.SWIMBA_OP_LINATTN_FWD)
+    S.check(S.swimba_linattn_fwd(dims, q, k, k, g, None, start, o, end, ws, ws.numel()))
+    tol = 3e-6 if B == 2 else 2.0 ** -20
+    assert mean_drift(end, start, g, L) < tol
+    ws = S.new_linattn_workspace(dims, S.SWIMBA_OP_LINATTN_BWD)
+    grads = [torch.empty_like(q) for _ in range(3)]
+    S.check(S.swimba_linattn_bwd(dims, q, k, k, g, None, None, k, start, *grads, end, ws, ws.numel()))
+    assert mean_drift(end, start, g, L) < tol
