@@ -446,7 +446,8 @@ swimba_status swimba_block_step(const swimba_block_dims *bd, const void *u,
  * bf16: chunks of 128 tokens on the tensor cores; the masked, decayed scores and the state's copy
  * for the readout are rounded to bf16 once each, everything that is carried on stays fp32 (values
  * enter the state update as two or three bf16 parts: 24 bits where S_final or dS0 is asked for and the
- * decay to it is above 2^-6, else 16). fp32, and bf16 of at most 8 tokens: the recurrence in fp32 on
+ * decay to it is above 2^-6, else 16). A state's decay is kept to more than fp32's bits over the
+ * tokens that it outlives, so that prompts and single tokens agree at slow decays. fp32, and bf16 of at most 8 tokens: the recurrence in fp32 on
  * the SIMT cores. A value that is not finite may spread to every output of its chunk of 128
  * tokens and to what follows it in its sequence (for the gradients of keys and values: to what
  * precedes it), never to another sequence. Outputs overlap nothing but what is said below. */
@@ -517,7 +518,8 @@ swimba_status swimba_linattn_bwd(const swimba_linattn_dims *dims, const void *q,
  *                                                     y NULL: h = res_scale res)
  *   n = h / sqrt(mean(h^2) + eps) w_pre               norm before the next block
  * With gate_last = 1 the gate follows the norm: p = y / sqrt(mean(y^2) + eps) w_post SiLU(z). All
- * arithmetic is fp32; n is taken from h before h is rounded to res_dtype. */
+ * arithmetic is fp32 (the gate's exponential and reciprocal are the approximate instructions, each
+ * within 2^-22); n is taken from h before h is rounded to res_dtype. */
 typedef struct {
   int64_t rows;      /* tokens */
   int32_t width;     /* channels: a multiple of 8, at most 16384 */

@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(256) la_rows_kernel(const __grid_constant__ La
 
 // ---- decode step ----------------------------------------------------------------------------------------
 // One CTA per (sequence, head) and `cols` columns: the state is read and written once (8 d_k d_v bytes),
-// which bounds it: 512 MiB of state, bf16 tokens, in 164 us, the measured copy rate. Threads go over the state
+// which bounds it: 512 MiB of state, bf16 tokens, in 163 us, the measured copy rate. Threads go over the state
 // row by row, 16 bytes each; the partial readouts of the threads that share columns meet in shared memory.
 // Few heads are cut into 32 columns (128 bytes of a row), so that every SM has a share: 96 heads of 128 x 128
 // take 4.1 us, 6.2 whole. Many heads stay whole, rows of 512 bytes; a call of a few heads is bound by its launch.
@@ -428,8 +428,11 @@ struct LaLayout {
 };
 
 // bf16 sequences of a few tokens take the recurrence too: a chunk costs the same however few it holds, and nothing
-// but the output is rounded. Chunk against recurrence, 64 sequences x 32 heads of 128 forward, 128 x 32 backward:
-// 4 tokens 134 against 96 us and 510 against 264, 8 tokens 134 / 115 and 510 / 402, 16 tokens 134 / 161 and 510 / 684.
+// but the output is rounded. Chunk against recurrence, forward and backward, us of the kernels:
+//   64 sequences x 32 heads of 128: 2 tokens 104 / 73 and 257 / 107, 8 tokens 105 / 100 and 257 / 197, 16 tokens
+//   105 / 142 and 259 / 339; 4 x 24 heads of 128: 8 tokens 10.5 / 10.6 and 16 / 11, 16 tokens 10.5 / 14.7 and 16 / 18
+//   64 x 32 heads of 64: 8 tokens 95 / 30 and 253 / 65; 4 x 24: 8.4 / 6.3 and 14 / 6.5; 1 x 8: 7.7 / 6.3 and 7.4 / 5.6
+// (heads of 64 would gain from it up to 16 tokens and more; heads of 128 lose).
 constexpr int kLaShort = 8;
 static_assert(kLaShort <= kLaSimtChunk, "bf16 sequences on the SIMT cores have one segment");
 bool la_use_tc(const swimba_linattn_dims* d) { return d->io_dtype == SWIMBA_BF16 && d->seqlen > kLaShort; }

@@ -105,7 +105,8 @@ struct LaSmem {
   static_assert(NW + 2 <= FACTORS);
   static constexpr int BYTES = FACTOR + FACTORS * 4;
   // Registers per thread of the six warpgroups (0-3, 4-7 and 8-11, 12-15, 16-19 and 20-23). A spill in one of
-  // the chunk loops costs several percent.
+  // the chunk loops costs several percent. With DX = 128 (outputs) 18 to 24 words are spilled all the same: given more
+  // registers each in turn, two thirds of the stores go with the state's warps, the rest with warps 0-3 and 4-11.
   static constexpr int REG_UTIL = DX == 128 ? 48 : DW == 128 ? 72 : 48, REG_PO = DX == 128 ? 64 : DW == 128 ? 72 : 80,
                        REG_M = DX == 128 ? 176 : DW == 128 ? 120 : 144, REG_W = DX == 128 ? 64 : DW == 128 ? 72 : 64;
   static_assert(REG_UTIL + 2 * REG_PO + REG_M + 2 * REG_W <= 6 * 80, "what the launch's 80 registers per thread allow");

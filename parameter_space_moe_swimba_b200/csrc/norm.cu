@@ -16,7 +16,9 @@
 // one warp (up to 256 channels) or one CTA of up to 512 threads, which walks its rows with the next ones
 // on their way: each thread copies the vectors of 8 channels that it will work on into shared memory of
 // its own (cp.async, no barrier), as many rows ahead as fit, and keeps its channels' weights and their gradients in
-// registers. Without the copies a row's loads waited for the row before it (16384 rows of 4096, bf16
+// registers. (Above 8192 channels a thread has 32, and the backward's 128 registers do not hold them: 1.2 KB of them
+// and of the row's values per thread go to local memory; 2048 rows of 16384 in bf16 take 316 to 425 us for 82 of
+// bytes, in fp32 500 for 164.) Without the copies a row's loads waited for the row before it (16384 rows of 4096, bf16
 // with an fp32 residual, backward: 547 us, 2.7 TB/s); with 8 channels per thread a third of the
 // instructions were the row's sums and addresses, so a thread takes 16 where rows are long. Now that backward
 // takes 389 us (3.8 TB/s, 58 % of the measured copy rate: 1300 instructions per warp and row at 40 % of the
