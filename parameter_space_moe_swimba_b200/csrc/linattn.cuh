@@ -60,18 +60,22 @@ __device__ __forceinline__ float la_pow(float lg, int e) { return e == 0 ? 1.f :
 
 // γ^e as hi + lo, for a factor that a state meets again and again: rounded once, a γ near 1 is off by up to 2^-25
 // at every use, with the same sign (4096 single tokens at a log decay of -1e-5: 6e-5 of the state; with lo 1e-8).
-// A γ^e below e^-1/2 is forgotten within a few uses.
+// A γ^e below e^-1/2 is forgotten within a few uses. lo has hi's sign and is not zero unless γ^e is (or nearly): an
+// infinite state then stays what it is.
 struct LaDecay {
   float hi, lo;
 };
 __device__ __forceinline__ LaDecay la_decay(float g, int e) {
   const float x = g * (float)e;
-  if (!(fabsf(x) < 0.5f)) return {la_pow(g * kLog2e, e), 0.f};
-  const float m = expm1f(x), hi = 1.f + m;
-  return {hi, m - (hi - 1.f)};  // exact: |m| < 1
+  if (!(fabsf(x) < 0.5f)) {
+    const float p = la_pow(g * kLog2e, e);
+    return {p, p * 0x1p-40f};
+  }
+  const float m = expm1f(x), hi = 1.f + m, lo = m - (hi - 1.f);  // exact: |m| < 1
+  return lo > 0.f ? LaDecay{hi, lo} : LaDecay{hi - 0x1p-24f, lo + 0x1p-24f};
 }
 
-// The j-th of a series of factors for hi + lo, 1/2 < hi <= 1: hi or hi ± 2^-24, whichever keeps the product of all of
+// The j-th of a series of factors for hi + lo, 1/2 < hi <= 1, |lo| <= 2^-24: hi or hi ± 2^-24, whichever keeps the product of all of
 // them next to the power. A function of j, so that a series may be taken up anywhere.
 __device__ __forceinline__ float la_factor(LaDecay d, int j) {
   const float c = d.lo * 0x1p24f;

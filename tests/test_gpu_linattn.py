@@ -505,3 +505,22 @@ def test_fp32_keeps_decays_next_to_one(S, B):
     grads = [torch.empty_like(q) for _ in range(3)]
     S.check(S.swimba_linattn_bwd(dims, q, k, k, g, None, None, k, start, *grads, end, ws, ws.numel()))
     assert mean_drift(end, start, g, L) < tol
+
+
+@pytest.mark.parametrize("decay", [0.0, -1e-5, -0.3, -0.7])
+def test_an_infinite_state_stays_infinite(S, decay):
+    """A single token, and segments that hand the state on: infinite elements stay what they are, the others too."""
+    for L in (1, 1500):
+        c = Case(17, 1, L, 1, 1, 64, 64, "bf16", decay=decay if L == 1 else decay / 500)
+        states = []
+        for _ in range(2):
+            o, end = torch.empty_like(c.q), torch.empty_like(c.S0)
+            if L == 1:
+                S.check(S.swimba_linattn_step(c.dims(S), c.q, c.k, c.v, c.g, c.S0, o, end))
+            else:
+                c.forward(S, o, end)
+            states.append(end)
+            c.S0[0, 0, 3, 5], c.S0[0, 0, 60, 1] = float("inf"), -float("inf")
+        want = states[0].clone()
+        want[0, 0, 3, 5], want[0, 0, 60, 1] = float("inf"), -float("inf")
+        assert torch.equal(states[1], want)
